@@ -293,6 +293,114 @@ cp_spec_status cp_spec_accept_batch(int32_t R, int32_t N, int32_t V, int32_t top
                                     const float* d_draft, int32_t* d_tokens, int32_t* d_n_accepted,
                                     int32_t* d_drafts, void* stream);
 
+/* ------------------------------------------------------ 4-bit operators
+ * Products with 4-bit weights, a KV cache held in 4 bits, and attention over
+ * it: the decoder's own operators for models whose weights and caches should
+ * take a quarter of the memory.  Context-free like cp_spec_accept_batch: no
+ * workspace, nothing kept between calls, asynchronous, safe to capture into a
+ * graph and to call from several threads and streams at once.  They run on the
+ * current device, which must be the pointers' and the stream's.
+ *
+ * The format.  A value is s * c, with c one of the sixteen E2M1 numbers +-0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6 and s the bfloat16 scale of a group of consecutive
+ * elements: s = bf16(max |x| / 6), c the E2M1 number nearest to x / s, ties to
+ * the even code, saturating at 6.  A group that holds an infinity or a NaN
+ * reads back as NaN; one whose scale rounds to zero reads back as zeros.
+ *
+ * Element types (dtype, out_dtype): 0 float32, 1 bfloat16, 2 float16.  Row
+ * strides count elements; a row itself is dense. */
+#define CP_SPEC_MAX_W4_K 32768
+#define CP_SPEC_MAX_KV4_ROWS 64
+
+/* Bytes of a packed matrix [n][k] (rows padded to 16, columns to 128 by
+ * zeros), 0 if the arguments are invalid.  n >= 1, 1 <= k <= CP_SPEC_MAX_W4_K,
+ * group 32, 64 or 128. */
+size_t cp_spec_w4_bytes(int32_t n, int32_t k, int32_t group);
+
+/* Quantises d_w [n][k] (row stride w_stride >= k) into d_packed
+ * (cp_spec_w4_bytes, 16-byte aligned), in groups along k.  Once per matrix;
+ * the layout is the library's own. */
+cp_spec_status cp_spec_w4_pack(int32_t n, int32_t k, int32_t group, int32_t dtype, const void* d_w, int64_t w_stride,
+                               void* d_packed, void* stream);
+
+/* The values a packed matrix stands for, rounded once to dtype: d_w (out) [n][k]. */
+cp_spec_status cp_spec_w4_unpack(int32_t n, int32_t k, int32_t group, int32_t dtype, const void* d_packed, void* d_w,
+                                 void* stream);
+
+/* y[r][i] = sum_j x[r][j] w[i][j] for `rows` rows (0 .. 65535) of x: the
+ * product of a decoder pass, made for the few rows of a verify window or a
+ * batch of streams (up to 32 rows, 16 of float32, share one read of w).
+ * d_x [rows][k] of dtype with row stride x_stride >= k, d_y (out) [rows][n] of
+ * out_dtype (dtype, or 0) with row stride y_stride >= n; nothing between the
+ * rows of d_y is written.  Sums in float32; float32 inputs count with 22 bits,
+ * the 16-bit types exactly (down to 2^-29 of the largest of 128 neighbours).
+ * The order of the sums depends on the shape only: a row's result does not
+ * depend on the values of the rows beside it. */
+cp_spec_status cp_spec_w4_gemv(int32_t rows, int32_t n, int32_t k, int32_t group, int32_t dtype, int32_t out_dtype,
+                               const void* d_x, int64_t x_stride, const void* d_packed, void* d_y, int64_t y_stride,
+                               void* stream);
+
+/* A KV cache in 4 bits: n_pages pages of page_size token slots (a multiple of
+ * 16) for n_kv_heads heads of head_dim channels (64, 128 or 256), one scale
+ * per 32 channels of a token and head, keys and values together.  The caller
+ * owns the memory (cp_spec_kv4_bytes, 16-byte aligned) and need not clear it.
+ *
+ * d_pages [n_seqs][max_pages] int32 maps page j of sequence b to a page of the
+ * cache; NULL: sequence b owns pages b * max_pages .. (needs n_seqs *
+ * max_pages <= n_pages).  max_pages * page_size < 2^31.  An entry outside
+ * [0, n_pages) is never followed: its positions are not written, read back as
+ * zeros, and are left out of the attention.  So are positions past max_pages *
+ * page_size. */
+typedef struct {
+  int32_t n_pages, page_size, n_kv_heads, head_dim;
+} cp_spec_kv4;
+
+/* Bytes of the cache, 0 if the shape is invalid. */
+size_t cp_spec_kv4_bytes(const cp_spec_kv4* shape);
+
+/* Quantises rows of keys and values as they are written: row i of sequence b
+ * goes to position d_pos[b] + i, for i < d_rows[b] (clamped to 0 .. rows; NULL:
+ * rows).  d_k, d_v [n_seqs * rows][n_kv_heads][head_dim] with row strides
+ * k_stride, v_stride >= n_kv_heads * head_dim (slices of a fused projection
+ * work).  Other slots keep their values.  Two rows written to one slot by
+ * calls or sequences that overlap in time leave it undefined; neighbouring
+ * slots may be written at the same time. */
+cp_spec_status cp_spec_kv4_append(const cp_spec_kv4* shape, void* d_cache, const int32_t* d_pages, int32_t max_pages,
+                                  int32_t n_seqs, int32_t rows, const int32_t* d_pos, const int32_t* d_rows, int32_t dtype,
+                                  const void* d_k, int64_t k_stride, const void* d_v, int64_t v_stride, void* stream);
+
+/* The values the cache holds for positions 0 .. length - 1 of each sequence,
+ * rounded once to dtype: d_k, d_v (out) [n_seqs][length][n_kv_heads][head_dim].
+ * Positions at or past d_len[b] (NULL: length) read as zeros. */
+cp_spec_status cp_spec_kv4_read(const cp_spec_kv4* shape, const void* d_cache, const int32_t* d_pages, int32_t max_pages,
+                                int32_t n_seqs, int32_t length, const int32_t* d_len, int32_t dtype, void* d_k, void* d_v,
+                                void* stream);
+
+/* Attention of a window of rows over the held cache.  Sequence b has
+ * d_kv_len[b] positions (clamped to 0 .. max_pages * page_size), the last
+ * d_rows[b] of them (clamped to 0 .. rows; NULL: rows; rows <=
+ * CP_SPEC_MAX_KV4_ROWS) the window's own, already appended.  With base =
+ * d_kv_len[b] - d_rows[b], row i sees every position below base, and of the
+ * window the positions base .. base + i (d_mask NULL: causal) or base + j for
+ * every bit j of d_mask[b][i] (uint64; the nodes of a sparse tree set their
+ * ancestors' bits and their own).  Negative positions do not exist (base may
+ * be negative).
+ *   o = softmax(scale * q k^T) v,  scale finite,
+ * d_q, d_o (out) [n_seqs * rows][n_q_heads][head_dim] of dtype with row strides
+ * q_stride, o_stride >= n_q_heads * head_dim; query head e reads KV head
+ * e / (n_q_heads / n_kv_heads).  d_lse (optional, out) [n_seqs][rows][n_q_heads]
+ * float32: the log of the sum of the exponentials.  A row that sees nothing
+ * gives zeros and -infinity; a position that a row does not see cannot reach it,
+ * whatever is stored there.  Rows at or past d_rows[b] are left as they were.
+ * Results do not depend on timing; they do not depend on the other sequences,
+ * but max_pages and the numbers of sequences and rows choose how a long
+ * sequence is split, which moves them within rounding. */
+cp_spec_status cp_spec_kv4_attention(const cp_spec_kv4* shape, const void* d_cache, const int32_t* d_pages, int32_t max_pages,
+                                     int32_t n_seqs, int32_t rows, int32_t n_q_heads, const int32_t* d_kv_len,
+                                     const int32_t* d_rows, const uint64_t* d_mask, float scale, int32_t dtype,
+                                     const void* d_q, int64_t q_stride, void* d_o, int64_t o_stride, float* d_lse,
+                                     void* stream);
+
 /* Decode without any allocation: cp_spec_decode_frames for a one-off job,
  * with no context and no caller workspace.  The pages describe no such call;
  * it exists for callers that cannot allocate device memory when they decode:
@@ -363,8 +471,8 @@ cp_spec_status cp_spec_test_hooks(cp_spec_ctx* ctx, uint64_t wait_limit_ns, int3
 /* Number of launches the library has enqueued on this context: kernels
  * launched directly, plus one per launch of the context's call graph (whose
  * pass kernels are counted on the device: cp_spec_stats.kernel_launches).
- * cp_spec_accept_batch and cp_spec_decode_frames_static count in a
- * process-wide counter, ctx = NULL. */
+ * cp_spec_accept_batch, the 4-bit operators and cp_spec_decode_frames_static
+ * count in a process-wide counter, ctx = NULL. */
 int64_t cp_spec_launch_count(const cp_spec_ctx* ctx);
 
 /* Last error message of the context (or of the last context-free call when

@@ -26,7 +26,10 @@ EXPORTS = ("cp_spec_workspace_bytes", "cp_spec_init", "cp_spec_set_stream_sampli
            "cp_spec_begin_frame", "cp_spec_round", "cp_spec_teacher_logits", "cp_spec_accept_batch",
            "cp_spec_status_word", "cp_spec_read_stats", "cp_spec_reset_stats", "cp_spec_launch_count",
            "cp_spec_last_error", "cp_spec_destroy", "cp_spec_decode_frames_static", "cp_spec_test_hooks",
-           "cp_spec_workspace_bytes_tree", "cp_spec_init_tree")
+           "cp_spec_workspace_bytes_tree", "cp_spec_init_tree", "cp_spec_w4_bytes", "cp_spec_w4_pack",
+           "cp_spec_w4_unpack", "cp_spec_w4_gemv", "cp_spec_kv4_bytes", "cp_spec_kv4_append", "cp_spec_kv4_read",
+           "cp_spec_kv4_attention")
+MAX_W4_K, MAX_KV4_ROWS = 32768, 64
 
 
 class CpSpecError(RuntimeError):
@@ -55,6 +58,10 @@ class Config(C.Structure):
 
 class Tree(C.Structure):
     _fields_ = [("n", C.c_int32), ("parent", C.c_void_p), ("rank", C.c_void_p)]
+
+
+class Kv4(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("n_pages", "page_size", "n_kv_heads", "head_dim")]
 
 
 class Stats(C.Structure):
@@ -94,6 +101,17 @@ def load():
     L.cp_spec_teacher_logits.argtypes = [vp, i32, i32, vp, vp, vp, vp, vp]
     L.cp_spec_accept_batch.argtypes = [i32, i32, i32, i32, f32, u64, i32, vp, vp, vp, vp, vp, vp]
     L.cp_spec_decode_frames_static.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
+    i64 = C.c_int64
+    L.cp_spec_w4_bytes.argtypes = [i32, i32, i32]
+    L.cp_spec_w4_bytes.restype = sz
+    L.cp_spec_w4_pack.argtypes = [i32, i32, i32, i32, vp, i64, vp, vp]
+    L.cp_spec_w4_unpack.argtypes = [i32, i32, i32, i32, vp, vp, vp]
+    L.cp_spec_w4_gemv.argtypes = [i32, i32, i32, i32, i32, i32, vp, i64, vp, vp, i64, vp]
+    L.cp_spec_kv4_bytes.argtypes = [vp]
+    L.cp_spec_kv4_bytes.restype = sz
+    L.cp_spec_kv4_append.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, i64, vp, i64, vp]
+    L.cp_spec_kv4_read.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, vp, vp, vp]
+    L.cp_spec_kv4_attention.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, f32, i32, vp, i64, vp, i64, vp, vp]
     L.cp_spec_status_word.argtypes = [vp, vp]
     L.cp_spec_test_hooks.argtypes = [vp, u64, i32]
     L.cp_spec_read_stats.argtypes = [vp, vp, vp]
@@ -106,7 +124,9 @@ def load():
     L.cp_spec_destroy.restype = None
     for name in ("cp_spec_init", "cp_spec_init_tree", "cp_spec_set_stream_sampling", "cp_spec_decode_frames", "cp_spec_begin_frame",
                  "cp_spec_round", "cp_spec_teacher_logits", "cp_spec_accept_batch", "cp_spec_status_word",
-                 "cp_spec_read_stats", "cp_spec_reset_stats", "cp_spec_decode_frames_static", "cp_spec_test_hooks"):
+                 "cp_spec_read_stats", "cp_spec_reset_stats", "cp_spec_decode_frames_static", "cp_spec_test_hooks", "cp_spec_w4_pack",
+                 "cp_spec_w4_unpack", "cp_spec_w4_gemv", "cp_spec_kv4_append", "cp_spec_kv4_read",
+                 "cp_spec_kv4_attention"):
         getattr(L, name).restype = C.c_int
     _lib = L
     return L
@@ -309,3 +329,173 @@ def decode_frames_static(spec: synth.ModelSpec, device_weights: dict, verify_win
                                           _ptr(x), _ptr(c0), _ptr(codes), _ptr(status), _stream())
     _check(rc, None, allow=(OK, W_AR_FALLBACK))
     return codes, rc
+
+
+# ------------------------------------------------------- 4-bit operators
+_DTYPES = None  # torch dtype -> element type of the C ABI (torch is imported on first use)
+
+
+def _elem_type(dtype) -> int:
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise CpSpecError(E_INVALID, f"element type {dtype}: float32, bfloat16 or float16 wanted")
+    return code
+
+
+def _stream_of(t) -> int:
+    """The current stream, after a check that t lives on the current CUDA device (the library launches there)."""
+    import torch
+    dev = t.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise CpSpecError(E_INVALID, f"tensor on {dev}: the library runs on the current CUDA device")
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise CpSpecError(E_INVALID, what)
+
+
+def _index(t, n: int, what: str, like) -> int:
+    """Pointer of a dense int32 tensor of n elements beside `like`, or 0 for None."""
+    if t is None:
+        return 0
+    import torch
+    _need(t.dtype == torch.int32 and t.numel() == n and t.is_contiguous() and t.device == like.device,
+          f"{what}: {n} dense int32 values on {like.device} wanted")
+    return t.data_ptr()
+
+
+def _row_stride(t, what: str) -> int:
+    """Elements between the rows of t [n_seqs, rows, heads, head_dim]: its last two axes dense, its first two one axis."""
+    b, m, h, d = t.shape
+    st = t.stride()
+    _need((d == 1 or st[3] == 1) and (h == 1 or st[2] == d) and (b == 1 or m == 1 or st[0] == m * st[1]),
+          f"{what}: rows [heads, head_dim] must be dense and evenly spaced")
+    return max(st[1] if m > 1 else (st[0] if b > 1 else h * d), 0)
+
+
+class W4Matrix:
+    """A weight matrix [n, k] packed by w4_pack (data: the library's own layout)."""
+
+    def __init__(self, n: int, k: int, group: int, data):
+        self.n, self.k, self.group, self.data = n, k, group, data
+
+
+def w4_pack(w, group: int = 32) -> W4Matrix:
+    """Quantise w [n, k] (float32, bfloat16 or float16, rows dense) to 4 bits with a scale per `group` columns."""
+    import torch
+    lib = load()
+    _need(w.dim() == 2 and (w.shape[1] <= 1 or w.stride(1) == 1), "w: a matrix with dense rows wanted")
+    n, k = w.shape
+    stream, code = _stream_of(w), _elem_type(w.dtype)
+    nbytes = lib.cp_spec_w4_bytes(n, k, group)
+    if nbytes == 0:
+        _check(E_INVALID)
+    out = W4Matrix(n, k, group, torch.empty(nbytes, dtype=torch.uint8, device=w.device))
+    _check(lib.cp_spec_w4_pack(n, k, group, code, w.data_ptr(), w.stride(0) if n > 1 else k, out.data.data_ptr(), stream))
+    return out
+
+
+def w4_unpack(w: W4Matrix, dtype=None):
+    """The values [n, k] that a packed matrix stands for (float32 unless dtype says otherwise)."""
+    import torch
+    out = torch.empty((w.n, w.k), dtype=dtype or torch.float32, device=w.data.device)
+    _check(load().cp_spec_w4_unpack(w.n, w.k, w.group, _elem_type(out.dtype), w.data.data_ptr(), out.data_ptr(),
+                                    _stream_of(w.data)))
+    return out
+
+
+def w4_gemv(x, w: W4Matrix, out=None, out_dtype=None):
+    """x [rows, k] times the packed matrix: [rows, n] of x's type (or float32; asynchronous)."""
+    import torch
+    _need(x.dim() == 2 and x.shape[1] == w.k and (w.k == 1 or x.stride(1) == 1), f"x: [rows, {w.k}] with dense rows wanted")
+    rows = x.shape[0]
+    if out is None:
+        out = torch.empty((rows, w.n), dtype=out_dtype or x.dtype, device=x.device)
+    else:
+        _need(out.shape == (rows, w.n) and (w.n == 1 or out.stride(1) == 1) and out.device == x.device
+              and (out_dtype is None or out.dtype == out_dtype), f"out: [{rows}, {w.n}] with dense rows beside x wanted")
+    _need(w.data.device == x.device, "x and the packed matrix on one device wanted")
+    _check(load().cp_spec_w4_gemv(rows, w.n, w.k, w.group, _elem_type(x.dtype), _elem_type(out.dtype), x.data_ptr(),
+                                  x.stride(0) if rows > 1 else w.k, w.data.data_ptr(), out.data_ptr(),
+                                  out.stride(0) if rows > 1 else w.n, _stream_of(x)))
+    return out
+
+
+class Kv4Cache:
+    """Keys and values held in 4 bits, in n_pages pages of page_size token slots.
+
+    pages (int32 [n_seqs, max_pages]) maps the positions of each sequence to pages; without it
+    sequence b owns n_pages // n_seqs neighbouring pages.  The memory starts as zeros."""
+
+    def __init__(self, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, device="cuda"):
+        import torch
+        self.shape = Kv4(n_pages, page_size, n_kv_heads, head_dim)
+        self._shape = C.addressof(self.shape)
+        nbytes = load().cp_spec_kv4_bytes(self._shape)
+        if nbytes == 0:
+            _check(E_INVALID)
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = n_pages, page_size, n_kv_heads, head_dim
+        self.data = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+    def _pages(self, pages, n_seqs: int):
+        """Pointer of the page table and pages per sequence."""
+        if pages is None:
+            return 0, self.n_pages // max(n_seqs, 1)
+        _need(pages.dim() == 2 and pages.shape[0] == n_seqs, f"pages: [{n_seqs}, max_pages] wanted")
+        return _index(pages, pages.numel(), "pages", self.data), pages.shape[1]
+
+    def append(self, k, v, pos, pages=None, n_rows=None):
+        """Write rows k, v [n_seqs, rows, n_kv_heads, head_dim]: row i of sequence b at position pos[b] + i (i < n_rows[b])."""
+        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and tuple(k.shape[2:]) == (self.n_kv_heads, self.head_dim)
+              and k.device == v.device == self.data.device,
+              f"k, v: [n_seqs, rows, {self.n_kv_heads}, {self.head_dim}] of one type beside the cache wanted")
+        b, m = k.shape[:2]
+        table, per = self._pages(pages, b)
+        _check(load().cp_spec_kv4_append(self._shape, self.data.data_ptr(), table, per, b, m, _index(pos, b, "pos", k),
+                                         _index(n_rows, b, "n_rows", k), _elem_type(k.dtype), k.data_ptr(),
+                                         _row_stride(k, "k"), v.data_ptr(), _row_stride(v, "v"), _stream_of(k)))
+
+    def read(self, length: int, pages=None, lens=None, n_seqs=None, dtype=None):
+        """Keys and values of positions 0 .. length - 1: two tensors [n_seqs, length, n_kv_heads, head_dim].
+
+        Positions at or past lens[b] read as zeros."""
+        import torch
+        b = n_seqs if n_seqs is not None else (pages.shape[0] if pages is not None else 1)
+        table, per = self._pages(pages, b)
+        k, v = (torch.empty((b, length, self.n_kv_heads, self.head_dim), dtype=dtype or torch.float32,
+                            device=self.data.device) for _ in range(2))
+        _check(load().cp_spec_kv4_read(self._shape, self.data.data_ptr(), table, per, b, length, _index(lens, b, "lens", k),
+                                       _elem_type(k.dtype), k.data_ptr(), v.data_ptr(), _stream_of(self.data)))
+        return k, v
+
+    def attention(self, q, kv_len, pages=None, n_rows=None, mask=None, scale=None, out=None, want_lse=False):
+        """Attention of q [n_seqs, rows, n_q_heads, head_dim] over the cache (see cp_spec_kv4_attention).
+
+        kv_len int32 [n_seqs] counts the window's own rows, mask int64 [n_seqs, rows] holds the bits of the window
+        rows that a row sees (None: causal), scale is head_dim ** -0.5 unless given.  Returns the output, and with
+        want_lse also the log of the sums of exponentials [n_seqs, rows, n_q_heads] (rows past n_rows[b] are not written)."""
+        import torch
+        _need(q.dim() == 4 and q.shape[3] == self.head_dim and q.device == self.data.device,
+              f"q: [n_seqs, rows, n_q_heads, {self.head_dim}] beside the cache wanted")
+        b, m, nq, d = q.shape
+        if out is None:
+            out = torch.empty((b, m, nq, d), dtype=q.dtype, device=q.device)
+        else:
+            _need(out.shape == q.shape and out.dtype == q.dtype and out.device == q.device, "out: q's shape, type and device wanted")
+        if mask is not None:
+            _need(mask.dtype == torch.int64 and tuple(mask.shape) == (b, m) and mask.is_contiguous()
+                  and mask.device == q.device, f"mask: dense int64 [{b}, {m}] wanted")
+        lse = torch.empty((b, m, nq), dtype=torch.float32, device=q.device) if want_lse else None
+        table, per = self._pages(pages, b)
+        _check(load().cp_spec_kv4_attention(self._shape, self.data.data_ptr(), table, per, b, m, nq,
+                                            _index(kv_len, b, "kv_len", q), _index(n_rows, b, "n_rows", q), _ptr(mask),
+                                            d ** -0.5 if scale is None else scale, _elem_type(q.dtype), q.data_ptr(),
+                                            _row_stride(q, "q"), out.data_ptr(), _row_stride(out, "out"), _ptr(lse),
+                                            _stream_of(q)))
+        return (out, lse) if want_lse else out

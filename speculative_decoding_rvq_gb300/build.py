@@ -17,7 +17,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libcpspec.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["cp_spec.cu", "cp_pass_kernels.cu", "cp_accept_kernel.cu"]
+SOURCES = ["cp_spec.cu", "cp_pass_kernels.cu", "cp_accept_kernel.cu", "cp_w4.cu", "cp_kv4.cu"]
 
 
 def _nvcc() -> str:
@@ -27,7 +27,7 @@ def _nvcc() -> str:
 
 def _inputs():
     return ([os.path.join(CSRC, s) for s in SOURCES] + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")))
+            + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def needs_build() -> bool:

@@ -18,6 +18,7 @@
 
 #include "../../include/cp_spec.h"
 #include "cp_frame.cuh"
+#include "cp_ops4.h"
 
 namespace cpk_host {
 cudaError_t configure_kernels(const cpk::FrameParams& P, int accept_warps);
@@ -703,6 +704,184 @@ cp_spec_status cp_spec_accept_batch(int32_t R, int32_t N, int32_t V, int32_t top
   if (e != cudaSuccess) return check_cuda(nullptr, e, "accept kernel launch");
   g_free_launches.fetch_add(1);
   return CP_SPEC_OK;
+}
+
+// ------------------------------------------------------- 4-bit operators
+namespace {
+
+bool dtype_ok(int32_t t) { return t >= 0 && t <= 2; }
+bool bad_ptr(const void* p) { return !p || !aligned16(p); }
+
+// SMs of the current device.
+cudaError_t device_sms(int* sms) {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && (*sms = cached[dev].load()) > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) cached[dev].store(*sms);
+  return e;
+}
+
+cp_spec_status launched(cudaError_t e, const char* what) {
+  if (e != cudaSuccess) {
+    cudaGetLastError();  // a refused launch is reported here and nowhere else
+    return check_cuda(nullptr, e, what);
+  }
+  g_free_launches.fetch_add(1);
+  return CP_SPEC_OK;
+}
+
+cp_spec_status check_w4(int32_t n, int32_t k, int32_t group) {
+  if (n < 1 || k < 1) return fail(nullptr, CP_SPEC_E_INVALID, "n and k must be >= 1");
+  if (k > CP_SPEC_MAX_W4_K) return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "k must be <= %d", CP_SPEC_MAX_W4_K);
+  if (group != 32 && group != 64 && group != 128) return fail(nullptr, CP_SPEC_E_INVALID, "group must be 32, 64 or 128");
+  if (n > (1 << 30)) return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "n must be <= 2^30");
+  return CP_SPEC_OK;
+}
+
+cp_spec_status check_kv4(const cp_spec_kv4* S) {
+  if (!S) return fail(nullptr, CP_SPEC_E_INVALID, "null cache shape");
+  if (S->n_pages < 1 || S->n_kv_heads < 1) return fail(nullptr, CP_SPEC_E_INVALID, "n_pages and n_kv_heads must be >= 1");
+  if (S->n_kv_heads > 1024) return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "n_kv_heads must be <= 1024");
+  if (S->page_size < 16 || S->page_size % 16 || S->page_size > (1 << 20))
+    return fail(nullptr, CP_SPEC_E_INVALID, "page_size must be a multiple of 16 in [16, 2^20]");
+  if (S->head_dim != 64 && S->head_dim != 128 && S->head_dim != 256)
+    return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "head_dim must be 64, 128 or 256");
+  return CP_SPEC_OK;
+}
+
+// The parts that every call on a cache shares.
+cp_spec_status check_kv4_call(const cp_spec_kv4* S, const void* cache, const int32_t* pages, int32_t max_pages, int32_t n_seqs,
+                              int32_t rows, int32_t dtype) {
+  cp_spec_status v = check_kv4(S);
+  if (v != CP_SPEC_OK) return v;
+  if (!dtype_ok(dtype)) return fail(nullptr, CP_SPEC_E_INVALID, "dtype must be 0 (fp32), 1 (bf16) or 2 (fp16)");
+  if (n_seqs < 0 || rows < 0) return fail(nullptr, CP_SPEC_E_INVALID, "n_seqs and the number of rows must be >= 0");
+  if (max_pages < 1 || (long long)max_pages * S->page_size > 0x7FFFFFFFll)
+    return fail(nullptr, CP_SPEC_E_INVALID, "max_pages must be >= 1 with max_pages * page_size below 2^31");
+  if (bad_ptr(cache) || (pages && !aligned16(pages))) return fail(nullptr, CP_SPEC_E_INVALID, "cache or page table null or misaligned");
+  if (!pages && (long long)n_seqs * max_pages > S->n_pages)
+    return fail(nullptr, CP_SPEC_E_INVALID, "without a page table n_seqs * max_pages must not exceed n_pages");
+  if ((long long)n_seqs * ((long long)rows / 2 + 1) > (1ll << 38) / ((long long)S->n_kv_heads * S->head_dim))
+    return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "too many rows for one launch");
+  return CP_SPEC_OK;
+}
+
+cpk_host::Kv4Shape kv4_shape(const cp_spec_kv4* S) {
+  return cpk_host::Kv4Shape{S->n_pages, S->page_size, S->n_kv_heads, S->head_dim};
+}
+
+}  // namespace
+
+size_t cp_spec_w4_bytes(int32_t n, int32_t k, int32_t group) {
+  return check_w4(n, k, group) == CP_SPEC_OK ? cpk_host::w4_bytes(n, k, group) : 0;
+}
+
+cp_spec_status cp_spec_w4_pack(int32_t n, int32_t k, int32_t group, int32_t dtype, const void* d_w, int64_t w_stride,
+                               void* d_packed, void* stream) {
+  cp_spec_status v = check_w4(n, k, group);
+  if (v != CP_SPEC_OK) return v;
+  if (!dtype_ok(dtype)) return fail(nullptr, CP_SPEC_E_INVALID, "dtype must be 0 (fp32), 1 (bf16) or 2 (fp16)");
+  if (w_stride < k) return fail(nullptr, CP_SPEC_E_INVALID, "w_stride must be >= k");
+  if (bad_ptr(d_w) || bad_ptr(d_packed)) return fail(nullptr, CP_SPEC_E_INVALID, "null or misaligned pointer");
+  return launched(cpk_host::launch_w4_pack(n, k, group, dtype, d_w, w_stride, d_packed, static_cast<cudaStream_t>(stream)),
+                  "w4 pack launch");
+}
+
+cp_spec_status cp_spec_w4_unpack(int32_t n, int32_t k, int32_t group, int32_t dtype, const void* d_packed, void* d_w,
+                                 void* stream) {
+  cp_spec_status v = check_w4(n, k, group);
+  if (v != CP_SPEC_OK) return v;
+  if (!dtype_ok(dtype)) return fail(nullptr, CP_SPEC_E_INVALID, "dtype must be 0 (fp32), 1 (bf16) or 2 (fp16)");
+  if (bad_ptr(d_w) || bad_ptr(d_packed)) return fail(nullptr, CP_SPEC_E_INVALID, "null or misaligned pointer");
+  return launched(cpk_host::launch_w4_unpack(n, k, group, dtype, d_packed, d_w, static_cast<cudaStream_t>(stream)),
+                  "w4 unpack launch");
+}
+
+cp_spec_status cp_spec_w4_gemv(int32_t rows, int32_t n, int32_t k, int32_t group, int32_t dtype, int32_t out_dtype,
+                               const void* d_x, int64_t x_stride, const void* d_packed, void* d_y, int64_t y_stride,
+                               void* stream) {
+  cp_spec_status v = check_w4(n, k, group);
+  if (v != CP_SPEC_OK) return v;
+  if (rows < 0 || rows > 65535) return fail(nullptr, CP_SPEC_E_INVALID, "rows must be in [0, 65535]");
+  if (!dtype_ok(dtype) || (out_dtype != dtype && out_dtype != 0))
+    return fail(nullptr, CP_SPEC_E_INVALID, "dtype must be 0, 1 or 2, out_dtype the same or 0");
+  if (x_stride < k || y_stride < n) return fail(nullptr, CP_SPEC_E_INVALID, "row strides must cover a row");
+  if (rows == 0) return CP_SPEC_OK;
+  if (bad_ptr(d_x) || bad_ptr(d_packed) || bad_ptr(d_y)) return fail(nullptr, CP_SPEC_E_INVALID, "null or misaligned pointer");
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return check_cuda(nullptr, e, "device query");
+  return launched(cpk_host::launch_w4_gemv(rows, n, k, group, dtype, out_dtype, d_x, x_stride, d_packed, d_y, y_stride, sms,
+                                           static_cast<cudaStream_t>(stream)),
+                  "w4 gemv launch");
+}
+
+size_t cp_spec_kv4_bytes(const cp_spec_kv4* shape) {
+  if (check_kv4(shape) != CP_SPEC_OK) return 0;
+  return cpk_host::kv4_bytes(shape->n_pages, shape->page_size, shape->n_kv_heads, shape->head_dim);
+}
+
+cp_spec_status cp_spec_kv4_append(const cp_spec_kv4* shape, void* d_cache, const int32_t* d_pages, int32_t max_pages,
+                                  int32_t n_seqs, int32_t rows, const int32_t* d_pos, const int32_t* d_rows, int32_t dtype,
+                                  const void* d_k, int64_t k_stride, const void* d_v, int64_t v_stride, void* stream) {
+  cp_spec_status v = check_kv4_call(shape, d_cache, d_pages, max_pages, n_seqs, rows, dtype);
+  if (v != CP_SPEC_OK) return v;
+  const int64_t width = (int64_t)shape->n_kv_heads * shape->head_dim;
+  if (k_stride < width || v_stride < width) return fail(nullptr, CP_SPEC_E_INVALID, "row strides must cover a row");
+  if (n_seqs == 0 || rows == 0) return CP_SPEC_OK;
+  if (bad_ptr(d_pos) || (d_rows && !aligned16(d_rows)) || bad_ptr(d_k) || bad_ptr(d_v))
+    return fail(nullptr, CP_SPEC_E_INVALID, "null or misaligned pointer");
+  return launched(cpk_host::launch_kv4_append(kv4_shape(shape), d_cache, d_pages, max_pages, n_seqs, rows, d_pos, d_rows, dtype,
+                                              d_k, k_stride, d_v, v_stride, static_cast<cudaStream_t>(stream)),
+                  "kv4 append launch");
+}
+
+cp_spec_status cp_spec_kv4_read(const cp_spec_kv4* shape, const void* d_cache, const int32_t* d_pages, int32_t max_pages,
+                                int32_t n_seqs, int32_t length, const int32_t* d_len, int32_t dtype, void* d_k, void* d_v,
+                                void* stream) {
+  cp_spec_status v = check_kv4_call(shape, d_cache, d_pages, max_pages, n_seqs, length, dtype);
+  if (v != CP_SPEC_OK) return v;
+  if (n_seqs == 0 || length == 0) return CP_SPEC_OK;
+  if ((d_len && !aligned16(d_len)) || bad_ptr(d_k) || bad_ptr(d_v))
+    return fail(nullptr, CP_SPEC_E_INVALID, "null or misaligned pointer");
+  return launched(cpk_host::launch_kv4_read(kv4_shape(shape), d_cache, d_pages, max_pages, n_seqs, length, d_len, dtype, d_k, d_v,
+                                            static_cast<cudaStream_t>(stream)),
+                  "kv4 read launch");
+}
+
+cp_spec_status cp_spec_kv4_attention(const cp_spec_kv4* shape, const void* d_cache, const int32_t* d_pages, int32_t max_pages,
+                                     int32_t n_seqs, int32_t rows, int32_t n_q_heads, const int32_t* d_kv_len,
+                                     const int32_t* d_rows, const uint64_t* d_mask, float scale, int32_t dtype,
+                                     const void* d_q, int64_t q_stride, void* d_o, int64_t o_stride, float* d_lse,
+                                     void* stream) {
+  cp_spec_status v = check_kv4_call(shape, d_cache, d_pages, max_pages, n_seqs, rows, dtype);
+  if (v != CP_SPEC_OK) return v;
+  if (rows > CP_SPEC_MAX_KV4_ROWS) return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "rows must be <= %d", CP_SPEC_MAX_KV4_ROWS);
+  if (n_q_heads < 1 || n_q_heads % shape->n_kv_heads || n_q_heads > 4096)
+    return fail(nullptr, CP_SPEC_E_INVALID, "n_q_heads must be a positive multiple of n_kv_heads, at most 4096");
+  if (!std::isfinite(scale)) return fail(nullptr, CP_SPEC_E_INVALID, "scale must be finite");
+  const int64_t width = (int64_t)n_q_heads * shape->head_dim;
+  if (q_stride < width || o_stride < width) return fail(nullptr, CP_SPEC_E_INVALID, "row strides must cover a row");
+  if (n_seqs == 0 || rows == 0) return CP_SPEC_OK;
+  if ((long long)n_seqs * rows * n_q_heads > (1ll << 27)) return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "too many query rows");
+  if (bad_ptr(d_kv_len) || (d_rows && !aligned16(d_rows)) || (d_mask && !aligned16(d_mask)) || bad_ptr(d_q) || bad_ptr(d_o) ||
+      (d_lse && !aligned16(d_lse)))
+    return fail(nullptr, CP_SPEC_E_INVALID, "null or misaligned pointer");
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return check_cuda(nullptr, e, "device query");
+  cpk_host::Kv4Attention A{};
+  A.cache = d_cache; A.pages = d_pages; A.kv_len = d_kv_len; A.n_rows = d_rows;
+  A.mask = reinterpret_cast<const unsigned long long*>(d_mask);
+  A.q = d_q; A.o = d_o; A.lse = d_lse;
+  A.qs = q_stride; A.os = o_stride;
+  A.max_pages = max_pages; A.B = n_seqs; A.M = rows; A.nq = n_q_heads; A.dtype = dtype;
+  A.scale = scale;
+  return launched(cpk_host::launch_kv4_attention(kv4_shape(shape), A, sms, static_cast<cudaStream_t>(stream)),
+                  "kv4 attention launch");
 }
 
 cp_spec_status cp_spec_decode_frames_static(const cp_spec_model* model, const cp_spec_weights* weights,
