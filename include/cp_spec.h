@@ -296,8 +296,8 @@ cp_spec_status cp_spec_accept_batch(int32_t R, int32_t N, int32_t V, int32_t top
 /* ------------------------------------------------------ 4-bit operators
  * Products with 4-bit weights, a KV cache held in 4 bits, and attention over
  * it: the decoder's own operators for models whose weights and caches should
- * take a quarter of the memory.  Context-free like cp_spec_accept_batch: no
- * workspace, nothing kept between calls, asynchronous, safe to capture into a
+ * take a quarter of the memory.  Context-free like cp_spec_accept_batch:
+ * nothing kept between calls, asynchronous, safe to capture into a
  * graph and to call from several threads and streams at once.  They run on the
  * current device, which must be the pointers' and the stream's.
  *
@@ -392,14 +392,21 @@ cp_spec_status cp_spec_kv4_read(const cp_spec_kv4* shape, const void* d_cache, c
  * float32: the log of the sum of the exponentials.  A row that sees nothing
  * gives zeros and -infinity; a position that a row does not see cannot reach it,
  * whatever is stored there.  Rows at or past d_rows[b] are left as they were.
- * Results do not depend on timing; they do not depend on the other sequences,
- * but max_pages and the numbers of sequences and rows choose how a long
- * sequence is split, which moves them within rounding. */
+ * Results do not depend on timing or on the other sequences' contents, but
+ * max_pages and the numbers of sequences, heads and rows choose how a long
+ * sequence is split, which moves them within rounding.
+ * d_work: cp_spec_kv4_attention_bytes of scratch (NULL where that is 0), used
+ * during the call's work only; calls that overlap in time need their own. */
 cp_spec_status cp_spec_kv4_attention(const cp_spec_kv4* shape, const void* d_cache, const int32_t* d_pages, int32_t max_pages,
                                      int32_t n_seqs, int32_t rows, int32_t n_q_heads, const int32_t* d_kv_len,
                                      const int32_t* d_rows, const uint64_t* d_mask, float scale, int32_t dtype,
                                      const void* d_q, int64_t q_stride, void* d_o, int64_t o_stride, float* d_lse,
-                                     void* stream);
+                                     void* d_work, size_t work_bytes, void* stream);
+
+/* Workspace of that call on the current device: 0 unless sequences are split
+ * (few sequences and heads, long tables); also 0 if the arguments are invalid. */
+size_t cp_spec_kv4_attention_bytes(const cp_spec_kv4* shape, int32_t max_pages, int32_t n_seqs, int32_t rows,
+                                   int32_t n_q_heads, int32_t dtype);
 
 /* Decode without any allocation: cp_spec_decode_frames for a one-off job,
  * with no context and no caller workspace.  The pages describe no such call;

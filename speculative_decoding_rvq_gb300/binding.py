@@ -28,7 +28,7 @@ EXPORTS = ("cp_spec_workspace_bytes", "cp_spec_init", "cp_spec_set_stream_sampli
            "cp_spec_last_error", "cp_spec_destroy", "cp_spec_decode_frames_static", "cp_spec_test_hooks",
            "cp_spec_workspace_bytes_tree", "cp_spec_init_tree", "cp_spec_w4_bytes", "cp_spec_w4_pack",
            "cp_spec_w4_unpack", "cp_spec_w4_gemv", "cp_spec_kv4_bytes", "cp_spec_kv4_append", "cp_spec_kv4_read",
-           "cp_spec_kv4_attention")
+           "cp_spec_kv4_attention", "cp_spec_kv4_attention_bytes")
 MAX_W4_K, MAX_KV4_ROWS = 32768, 64
 
 
@@ -111,7 +111,9 @@ def load():
     L.cp_spec_kv4_bytes.restype = sz
     L.cp_spec_kv4_append.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, i64, vp, i64, vp]
     L.cp_spec_kv4_read.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, vp, vp, vp]
-    L.cp_spec_kv4_attention.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, f32, i32, vp, i64, vp, i64, vp, vp]
+    L.cp_spec_kv4_attention.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, f32, i32, vp, i64, vp, i64, vp, vp, sz, vp]
+    L.cp_spec_kv4_attention_bytes.argtypes = [vp, i32, i32, i32, i32, i32]
+    L.cp_spec_kv4_attention_bytes.restype = sz
     L.cp_spec_status_word.argtypes = [vp, vp]
     L.cp_spec_test_hooks.argtypes = [vp, u64, i32]
     L.cp_spec_read_stats.argtypes = [vp, vp, vp]
@@ -126,7 +128,7 @@ def load():
                  "cp_spec_round", "cp_spec_teacher_logits", "cp_spec_accept_batch", "cp_spec_status_word",
                  "cp_spec_read_stats", "cp_spec_reset_stats", "cp_spec_decode_frames_static", "cp_spec_test_hooks", "cp_spec_w4_pack",
                  "cp_spec_w4_unpack", "cp_spec_w4_gemv", "cp_spec_kv4_append", "cp_spec_kv4_read",
-                 "cp_spec_kv4_attention"):
+                 "cp_spec_kv4_attention", "cp_spec_kv4_attention_bytes"):
         getattr(L, name).restype = C.c_int
     _lib = L
     return L
@@ -332,51 +334,58 @@ def decode_frames_static(spec: synth.ModelSpec, device_weights: dict, verify_win
 
 
 # ------------------------------------------------------- 4-bit operators
-_DTYPES = None  # torch dtype -> element type of the C ABI (torch is imported on first use)
+# These calls take a few microseconds on the device, so what they do here is kept short: no message is built
+# unless it is raised, and the stream comes as the raw handle of PyTorch's current stream.
+_torch = None
+_DTYPES = None  # torch dtype -> element type of the C ABI
+
+
+def _fast():
+    """The library and PyTorch, imported on first use."""
+    global _torch, _DTYPES
+    if _torch is None:
+        import torch
+        _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+        _torch = torch
+    return _lib or load()
+
+
+def _refuse(what: str):
+    raise CpSpecError(E_INVALID, what)
 
 
 def _elem_type(dtype) -> int:
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
     code = _DTYPES.get(dtype)
     if code is None:
-        raise CpSpecError(E_INVALID, f"element type {dtype}: float32, bfloat16 or float16 wanted")
+        _refuse(f"element type {dtype}: float32, bfloat16 or float16 wanted")
     return code
 
 
-def _stream_of(t) -> int:
-    """The current stream, after a check that t lives on the current CUDA device (the library launches there)."""
-    import torch
-    dev = t.device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise CpSpecError(E_INVALID, f"tensor on {dev}: the library runs on the current CUDA device")
-    return torch.cuda.current_stream().cuda_stream
+def _stream_on(dev: int) -> int:
+    """Handle of the current stream, after a check that `dev` (Tensor.get_device()) is the current CUDA device."""
+    if dev < 0 or dev != _torch._C._cuda_getDevice():
+        _refuse(f"tensor on device {dev}: the library runs on the current CUDA device")
+    return _torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise CpSpecError(E_INVALID, what)
-
-
-def _index(t, n: int, what: str, like) -> int:
-    """Pointer of a dense int32 tensor of n elements beside `like`, or 0 for None."""
+def _index(t, n: int, what: str, dev: int) -> int:
+    """Pointer of a dense int32 tensor of n elements on device dev, or 0 for None."""
     if t is None:
         return 0
-    import torch
-    _need(t.dtype == torch.int32 and t.numel() == n and t.is_contiguous() and t.device == like.device,
-          f"{what}: {n} dense int32 values on {like.device} wanted")
+    if t.dtype is not _torch.int32 or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(f"{what}: {n} dense int32 values beside the cache wanted")
     return t.data_ptr()
 
 
 def _row_stride(t, what: str) -> int:
     """Elements between the rows of t [n_seqs, rows, heads, head_dim]: its last two axes dense, its first two one axis."""
     b, m, h, d = t.shape
-    st = t.stride()
-    _need((d == 1 or st[3] == 1) and (h == 1 or st[2] == d) and (b == 1 or m == 1 or st[0] == m * st[1]),
-          f"{what}: rows [heads, head_dim] must be dense and evenly spaced")
-    return max(st[1] if m > 1 else (st[0] if b > 1 else h * d), 0)
+    if t.is_contiguous():
+        return h * d
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1 or (h > 1 and s2 != d) or (b > 1 and m > 1 and s0 != m * s1):
+        _refuse(f"{what}: rows [heads, head_dim] must be dense and evenly spaced")
+    return s1 if m > 1 else (s0 if b > 1 else h * d)
 
 
 class W4Matrix:
@@ -388,42 +397,52 @@ class W4Matrix:
 
 def w4_pack(w, group: int = 32) -> W4Matrix:
     """Quantise w [n, k] (float32, bfloat16 or float16, rows dense) to 4 bits with a scale per `group` columns."""
-    import torch
-    lib = load()
-    _need(w.dim() == 2 and (w.shape[1] <= 1 or w.stride(1) == 1), "w: a matrix with dense rows wanted")
+    lib = _fast()
+    if w.dim() != 2 or (w.shape[1] > 1 and w.stride(1) != 1):
+        _refuse("w: a matrix with dense rows wanted")
     n, k = w.shape
-    stream, code = _stream_of(w), _elem_type(w.dtype)
+    code, stream = _elem_type(w.dtype), _stream_on(w.get_device())
     nbytes = lib.cp_spec_w4_bytes(n, k, group)
     if nbytes == 0:
         _check(E_INVALID)
-    out = W4Matrix(n, k, group, torch.empty(nbytes, dtype=torch.uint8, device=w.device))
+    out = W4Matrix(n, k, group, _torch.empty(nbytes, dtype=_torch.uint8, device=w.device))
     _check(lib.cp_spec_w4_pack(n, k, group, code, w.data_ptr(), w.stride(0) if n > 1 else k, out.data.data_ptr(), stream))
     return out
 
 
 def w4_unpack(w: W4Matrix, dtype=None):
     """The values [n, k] that a packed matrix stands for (float32 unless dtype says otherwise)."""
-    import torch
-    out = torch.empty((w.n, w.k), dtype=dtype or torch.float32, device=w.data.device)
-    _check(load().cp_spec_w4_unpack(w.n, w.k, w.group, _elem_type(out.dtype), w.data.data_ptr(), out.data_ptr(),
-                                    _stream_of(w.data)))
+    lib = _fast()
+    stream = _stream_on(w.data.get_device())
+    out = _torch.empty((w.n, w.k), dtype=dtype or _torch.float32, device=w.data.device)
+    _check(lib.cp_spec_w4_unpack(w.n, w.k, w.group, _elem_type(out.dtype), w.data.data_ptr(), out.data_ptr(), stream))
     return out
 
 
 def w4_gemv(x, w: W4Matrix, out=None, out_dtype=None):
     """x [rows, k] times the packed matrix: [rows, n] of x's type (or float32; asynchronous)."""
-    import torch
-    _need(x.dim() == 2 and x.shape[1] == w.k and (w.k == 1 or x.stride(1) == 1), f"x: [rows, {w.k}] with dense rows wanted")
-    rows = x.shape[0]
+    lib = _lib if _torch is not None else _fast()
+    n, k, dt, dev, shape, st = w.n, w.k, x.dtype, x.get_device(), x.shape, x.stride()
+    if len(shape) != 2 or shape[1] != k or (st[1] != 1 and k > 1):
+        _refuse(f"x: [rows, {k}] with dense rows wanted")
+    rows = shape[0]
+    code, stream = _elem_type(dt), _stream_on(dev)
+    if w.data.get_device() != dev:
+        _refuse("x and the packed matrix on one device wanted")
     if out is None:
-        out = torch.empty((rows, w.n), dtype=out_dtype or x.dtype, device=x.device)
+        out_dtype = out_dtype or dt
+        out = _torch.empty((rows, n), dtype=out_dtype, device=x.device)
+        ys = n
     else:
-        _need(out.shape == (rows, w.n) and (w.n == 1 or out.stride(1) == 1) and out.device == x.device
-              and (out_dtype is None or out.dtype == out_dtype), f"out: [{rows}, {w.n}] with dense rows beside x wanted")
-    _need(w.data.device == x.device, "x and the packed matrix on one device wanted")
-    _check(load().cp_spec_w4_gemv(rows, w.n, w.k, w.group, _elem_type(x.dtype), _elem_type(out.dtype), x.data_ptr(),
-                                  x.stride(0) if rows > 1 else w.k, w.data.data_ptr(), out.data_ptr(),
-                                  out.stride(0) if rows > 1 else w.n, _stream_of(x)))
+        if (tuple(out.shape) != (rows, n) or (n > 1 and out.stride(1) != 1) or out.get_device() != dev
+                or (out_dtype is not None and out.dtype is not out_dtype)):
+            _refuse(f"out: [{rows}, {n}] with dense rows beside x wanted")
+        out_dtype = out.dtype
+        ys = out.stride(0) if rows > 1 else n
+    rc = lib.cp_spec_w4_gemv(rows, n, k, w.group, code, code if out_dtype is dt else _elem_type(out_dtype), x.data_ptr(),
+                             st[0] if rows > 1 else k, w.data.data_ptr(), out.data_ptr(), ys, stream)
+    if rc:
+        _check(rc)
     return out
 
 
@@ -434,44 +453,55 @@ class Kv4Cache:
     sequence b owns n_pages // n_seqs neighbouring pages.  The memory starts as zeros."""
 
     def __init__(self, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, device="cuda"):
-        import torch
+        lib = _fast()
         self.shape = Kv4(n_pages, page_size, n_kv_heads, head_dim)
         self._shape = C.addressof(self.shape)
-        nbytes = load().cp_spec_kv4_bytes(self._shape)
+        nbytes = lib.cp_spec_kv4_bytes(self._shape)
         if nbytes == 0:
             _check(E_INVALID)
         self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = n_pages, page_size, n_kv_heads, head_dim
-        self.data = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        self.data = _torch.zeros(nbytes, dtype=_torch.uint8, device=device)
 
-    def _pages(self, pages, n_seqs: int):
+    def _pages(self, pages, n_seqs: int, dev: int):
         """Pointer of the page table and pages per sequence."""
         if pages is None:
             return 0, self.n_pages // max(n_seqs, 1)
-        _need(pages.dim() == 2 and pages.shape[0] == n_seqs, f"pages: [{n_seqs}, max_pages] wanted")
-        return _index(pages, pages.numel(), "pages", self.data), pages.shape[1]
+        if pages.dim() != 2 or pages.shape[0] != n_seqs:
+            _refuse(f"pages: [{n_seqs}, max_pages] wanted")
+        return _index(pages, pages.numel(), "pages", dev), pages.shape[1]
 
     def append(self, k, v, pos, pages=None, n_rows=None):
         """Write rows k, v [n_seqs, rows, n_kv_heads, head_dim]: row i of sequence b at position pos[b] + i (i < n_rows[b])."""
-        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and tuple(k.shape[2:]) == (self.n_kv_heads, self.head_dim)
-              and k.device == v.device == self.data.device,
-              f"k, v: [n_seqs, rows, {self.n_kv_heads}, {self.head_dim}] of one type beside the cache wanted")
-        b, m = k.shape[:2]
-        table, per = self._pages(pages, b)
-        _check(load().cp_spec_kv4_append(self._shape, self.data.data_ptr(), table, per, b, m, _index(pos, b, "pos", k),
-                                         _index(n_rows, b, "n_rows", k), _elem_type(k.dtype), k.data_ptr(),
-                                         _row_stride(k, "k"), v.data_ptr(), _row_stride(v, "v"), _stream_of(k)))
+        lib, data = _fast(), self.data
+        shape, dev, dt = k.shape, data.get_device(), k.dtype
+        if (len(shape) != 4 or shape != v.shape or dt is not v.dtype or shape[2] != self.n_kv_heads
+                or shape[3] != self.head_dim or k.get_device() != dev or v.get_device() != dev):
+            _refuse(f"k, v: [n_seqs, rows, {self.n_kv_heads}, {self.head_dim}] of one type beside the cache wanted")
+        b = shape[0]
+        code, stream = _elem_type(dt), _stream_on(dev)
+        table, per = self._pages(pages, b, dev)
+        rc = lib.cp_spec_kv4_append(self._shape, data.data_ptr(), table, per, b, shape[1], _index(pos, b, "pos", dev),
+                                    _index(n_rows, b, "n_rows", dev), code, k.data_ptr(), _row_stride(k, "k"), v.data_ptr(),
+                                    _row_stride(v, "v"), stream)
+        if rc:
+            _check(rc)
 
     def read(self, length: int, pages=None, lens=None, n_seqs=None, dtype=None):
         """Keys and values of positions 0 .. length - 1: two tensors [n_seqs, length, n_kv_heads, head_dim].
 
         Positions at or past lens[b] read as zeros."""
-        import torch
+        lib, data = _fast(), self.data
+        dev = data.get_device()
+        stream = _stream_on(dev)
         b = n_seqs if n_seqs is not None else (pages.shape[0] if pages is not None else 1)
-        table, per = self._pages(pages, b)
-        k, v = (torch.empty((b, length, self.n_kv_heads, self.head_dim), dtype=dtype or torch.float32,
-                            device=self.data.device) for _ in range(2))
-        _check(load().cp_spec_kv4_read(self._shape, self.data.data_ptr(), table, per, b, length, _index(lens, b, "lens", k),
-                                       _elem_type(k.dtype), k.data_ptr(), v.data_ptr(), _stream_of(self.data)))
+        table, per = self._pages(pages, b, dev)
+        dtype = dtype or _torch.float32
+        size, code = (b, length, self.n_kv_heads, self.head_dim), _elem_type(dtype)
+        k, v = _torch.empty(size, dtype=dtype, device=data.device), _torch.empty(size, dtype=dtype, device=data.device)
+        rc = lib.cp_spec_kv4_read(self._shape, data.data_ptr(), table, per, b, length, _index(lens, b, "lens", dev), code,
+                                  k.data_ptr(), v.data_ptr(), stream)
+        if rc:
+            _check(rc)
         return k, v
 
     def attention(self, q, kv_len, pages=None, n_rows=None, mask=None, scale=None, out=None, want_lse=False):
@@ -480,22 +510,33 @@ class Kv4Cache:
         kv_len int32 [n_seqs] counts the window's own rows, mask int64 [n_seqs, rows] holds the bits of the window
         rows that a row sees (None: causal), scale is head_dim ** -0.5 unless given.  Returns the output, and with
         want_lse also the log of the sums of exponentials [n_seqs, rows, n_q_heads] (rows past n_rows[b] are not written)."""
-        import torch
-        _need(q.dim() == 4 and q.shape[3] == self.head_dim and q.device == self.data.device,
-              f"q: [n_seqs, rows, n_q_heads, {self.head_dim}] beside the cache wanted")
-        b, m, nq, d = q.shape
+        lib, data = _fast(), self.data
+        shape, dev, dt = q.shape, data.get_device(), q.dtype
+        if len(shape) != 4 or shape[3] != self.head_dim or q.get_device() != dev:
+            _refuse(f"q: [n_seqs, rows, n_q_heads, {self.head_dim}] beside the cache wanted")
+        b, m, nq, d = shape
+        code, stream = _elem_type(dt), _stream_on(dev)
         if out is None:
-            out = torch.empty((b, m, nq, d), dtype=q.dtype, device=q.device)
+            out = _torch.empty(shape, dtype=dt, device=data.device)
+            os = nq * d
         else:
-            _need(out.shape == q.shape and out.dtype == q.dtype and out.device == q.device, "out: q's shape, type and device wanted")
+            if out.shape != shape or out.dtype is not dt or out.get_device() != dev:
+                _refuse("out: q's shape, type and device wanted")
+            os = _row_stride(out, "out")
+        bits = 0
         if mask is not None:
-            _need(mask.dtype == torch.int64 and tuple(mask.shape) == (b, m) and mask.is_contiguous()
-                  and mask.device == q.device, f"mask: dense int64 [{b}, {m}] wanted")
-        lse = torch.empty((b, m, nq), dtype=torch.float32, device=q.device) if want_lse else None
-        table, per = self._pages(pages, b)
-        _check(load().cp_spec_kv4_attention(self._shape, self.data.data_ptr(), table, per, b, m, nq,
-                                            _index(kv_len, b, "kv_len", q), _index(n_rows, b, "n_rows", q), _ptr(mask),
-                                            d ** -0.5 if scale is None else scale, _elem_type(q.dtype), q.data_ptr(),
-                                            _row_stride(q, "q"), out.data_ptr(), _row_stride(out, "out"), _ptr(lse),
-                                            _stream_of(q)))
+            if (mask.dtype is not _torch.int64 or tuple(mask.shape) != (b, m) or not mask.is_contiguous()
+                    or mask.get_device() != dev):
+                _refuse(f"mask: dense int64 [{b}, {m}] wanted")
+            bits = mask.data_ptr()
+        lse = _torch.empty((b, m, nq), dtype=_torch.float32, device=data.device) if want_lse else None
+        table, per = self._pages(pages, b, dev)
+        need = lib.cp_spec_kv4_attention_bytes(self._shape, per, b, m, nq, code)
+        work = _torch.empty(need, dtype=_torch.uint8, device=data.device) if need else None  # (freed in stream order)
+        rc = lib.cp_spec_kv4_attention(self._shape, data.data_ptr(), table, per, b, m, nq, _index(kv_len, b, "kv_len", dev),
+                                       _index(n_rows, b, "n_rows", dev), bits, d ** -0.5 if scale is None else scale, code,
+                                       q.data_ptr(), _row_stride(q, "q"), out.data_ptr(), os,
+                                       lse.data_ptr() if want_lse else 0, work.data_ptr() if need else 0, need, stream)
+        if rc:
+            _check(rc)
         return (out, lse) if want_lse else out

@@ -13,10 +13,11 @@
 //           in the low nibble (the values' product sums over tokens, so a pair
 //           of tokens makes one fp16x2 operand);
 //   scales  [16 tokens][head_dim / 32] of the keys, then of the values.
-#include <cooperative_groups.h>
 #include <cuda_runtime.h>
+#include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cp_fp4.cuh"
 #include "cp_ops4.h"
@@ -27,13 +28,19 @@ constexpr int kKvGroup = 32;
 
 __host__ __device__ inline int kv4_tile_bytes(int d) { return 18 * d; }
 
-// Address of the tile that holds position `pos` of sequence b for head h, or
-// null where the position has no page.  *slot: the position's slot in the tile.
+// Where positions are: a position's page by the table, its tile within the page.
 struct Kv4Map {
   unsigned char* cache;
   const int* pages;  // [B][max_pages], or null: sequence b owns pages b * max_pages ..
   int max_pages, page_size, n_pages, nkv, d;
+  int tpp, tpp_shift;     // tiles per page, and its logarithm where it is a power of two (else -1)
+  long long page_stride;  // bytes
 };
+
+// Page index of a tile of the sequence (a division only where the page size is no power of two).
+__device__ __forceinline__ int kv4_page_of_tile(const Kv4Map& M, int tile) {
+  return M.tpp_shift >= 0 ? tile >> M.tpp_shift : tile / M.tpp;
+}
 
 __device__ __forceinline__ int kv4_page(const Kv4Map& M, int b, int at) {
   if (at >= M.max_pages) return -1;
@@ -42,7 +49,7 @@ __device__ __forceinline__ int kv4_page(const Kv4Map& M, int b, int at) {
 }
 
 __device__ __forceinline__ unsigned char* kv4_tile(const Kv4Map& M, int page, int h, int tile_in_page) {
-  return M.cache + (((long long)page * M.nkv + h) * (M.page_size >> 4) + tile_in_page) * kv4_tile_bytes(M.d);
+  return M.cache + page * M.page_stride + (h * M.tpp + tile_in_page) * kv4_tile_bytes(M.d);
 }
 
 // ------------------------------------------------------------ write, read
@@ -52,7 +59,7 @@ __device__ __forceinline__ unsigned char* kv4_tile(const Kv4Map& M, int page, in
 // value codes; where only one of its tokens is written the other's nibbles
 // are left by an atomic exclusive-or of the nibbles that change (another
 // sequence, or another call, may be writing them).  Bound by the bytes of the
-// rows.
+// rows once the quotients cost three instructions each.
 struct Kv4Rows {
   Kv4Map map;
   const void* k;
@@ -62,12 +69,16 @@ struct Kv4Rows {
   long long ks, vs;  // row strides in elements
   const int* pos;    // first position of each sequence (append), null in read
   const int* len;    // rows of each sequence that count, or null
-  int B, M, npairs, dtype;
+  int B, M, npairs, chunks, dtype;  // chunks: of 4 channels (read: 8), per row
   bool kvec, vvec;
 };
 
 // Quantises four channels; every lane of the warp takes part.  Returns the
-// codes, *scale the group's scale bits.
+// codes, *scale the group's scale bits.  The quotients by a scale of ordinary
+// size come from its correctly rounded reciprocal y by q = x y, q + (x - q s) y
+// with fused multiply-adds, which is the correctly rounded quotient (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990).
 __device__ __forceinline__ uint32_t kv4_quantise(float4 x, uint32_t* scale) {
   uint32_t m = max(max(__float_as_uint(x.x) & 0x7FFFFFFFu, __float_as_uint(x.y) & 0x7FFFFFFFu),
                    max(__float_as_uint(x.z) & 0x7FFFFFFFu, __float_as_uint(x.w) & 0x7FFFFFFFu));
@@ -75,8 +86,19 @@ __device__ __forceinline__ uint32_t kv4_quantise(float4 x, uint32_t* scale) {
   for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   *scale = fp4_scale_bits(__uint_as_float(m), m >= 0x7F800000u);
   const float s = bf16_bits_f32(*scale);
-  return float2_to_e2m1(fp4_quotient(x.x, s), fp4_quotient(x.y, s)) |
-         float2_to_e2m1(fp4_quotient(x.z, s), fp4_quotient(x.w, s)) << 8;
+  float q[4] = {x.x, x.y, x.z, x.w};
+  if (s > 0x1p-100f && s < 0x1p100f) {
+    const float y = __frcp_rn(s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = q[i] * y;
+      q[i] = fmaf(fmaf(-a, s, q[i]), y, a);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = fp4_quotient(q[i], s);
+  }
+  return float2_to_e2m1(q[0], q[1]) | float2_to_e2m1(q[2], q[3]) << 8;
 }
 
 // The four 4-bit codes of c spread to the low nibbles of four bytes.
@@ -87,64 +109,57 @@ __device__ __forceinline__ uint32_t spread_nibbles(uint32_t c) {
 
 __global__ void __launch_bounds__(256) kv4_append_kernel(const __grid_constant__ Kv4Rows P) {
   const Kv4Map& M = P.map;
-  const int chunks = M.nkv * M.d / 4, ng = M.d / kKvGroup;
-  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int chunk = (int)(id % chunks);
-  const long long rest = id / chunks;
-  const int pair = (int)(rest % P.npairs);
-  const long long bl = rest / P.npairs;
-  const int b = (int)min(bl, (long long)P.B - 1);
-  const int n = bl < P.B ? (P.len ? min(max(__ldg(P.len + b), 0), P.M) : P.M) : 0;
-  const int p0 = __ldg(P.pos + b);
-  const long long even = ((long long)(p0 >> 1) + pair) * 2;  // position of the pair's even token
-  float4 kx[2], vx[2];
-  bool on[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const long long m = even + e - p0;  // row of the window
-    on[e] = m >= 0 && m < n;
-    const long long row = (long long)b * P.M + m;
-    kx[e] = vx[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (on[e]) {
-      const int es = elem_bytes(P.dtype);
-      kx[e] = load4(static_cast<const unsigned char*>(P.k) + row * P.ks * es, P.dtype, 4 * chunk, 4 * chunk + 4, P.kvec);
-      vx[e] = load4(static_cast<const unsigned char*>(P.v) + row * P.vs * es, P.dtype, 4 * chunk, 4 * chunk + 4, P.vvec);
-    }
-  }
-  uint32_t kc[2], vc[2], ksc[2], vsc[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    kc[e] = kv4_quantise(kx[e], &ksc[e]);
-    vc[e] = kv4_quantise(vx[e], &vsc[e]);
-  }
-  if (even < 0 || (!on[0] && !on[1])) return;  // (positions are below 2^31: the launcher bounds max_pages * page_size)
-  const long long at = even / M.page_size;
-  if (at >= M.max_pages) return;
-  const int page = kv4_page(M, b, (int)at);
-  if (page < 0) return;
-  const int in_page = (int)(even - at * M.page_size);
+  const int ng = M.d / kKvGroup, es = elem_bytes(P.dtype);
+  const unsigned id = blockIdx.x * 256u + threadIdx.x, pair = id / (unsigned)P.chunks, chunk = id - pair * P.chunks;
   const int h = chunk / (M.d / 4), c4 = chunk - h * (M.d / 4), w = c4 >> 3, lane8 = c4 & 7;
-  unsigned char* tile = kv4_tile(M, page, h, in_page >> 4);
-  const int slot = in_page & 15;
+  for (int b = blockIdx.y; b < P.B; b += gridDim.y) {  // (the loop is uniform: the shuffles below see whole warps)
+    const int n = pair < (unsigned)P.npairs ? (P.len ? min(max(__ldg(P.len + b), 0), P.M) : P.M) : 0;
+    const int p0 = __ldg(P.pos + b);
+    const long long even = ((long long)(p0 >> 1) + pair) * 2;  // position of the pair's even token
+    float4 kx[2], vx[2];
+    bool on[2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    if (!on[e]) continue;
-    *reinterpret_cast<uint16_t*>(tile + (slot + e) * (M.d / 2) + (lane8 >> 1) * (ng * 4) + w * 4 + (lane8 & 1) * 2) =
-        (uint16_t)kc[e];
-    if (lane8 == 0) {
-      uint16_t* sc = reinterpret_cast<uint16_t*>(tile + 16 * M.d) + (slot + e) * ng + w;
-      sc[0] = (uint16_t)ksc[e];
-      sc[16 * ng] = (uint16_t)vsc[e];
+    for (int e = 0; e < 2; ++e) {
+      const long long m = even + e - p0;  // row of the window
+      on[e] = m >= 0 && m < n;
+      const long long row = (long long)b * P.M + m;
+      kx[e] = vx[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (on[e]) {
+        kx[e] = load4(static_cast<const unsigned char*>(P.k) + row * P.ks * es, P.dtype, 4 * chunk, 4 * chunk + 4, P.kvec);
+        vx[e] = load4(static_cast<const unsigned char*>(P.v) + row * P.vs * es, P.dtype, 4 * chunk, 4 * chunk + 4, P.vvec);
+      }
     }
-  }
-  uint32_t* vw = reinterpret_cast<uint32_t*>(tile + 8 * M.d + (slot >> 1) * M.d + lane8 * (ng * 4) + w * 4);
-  const uint32_t bits = spread_nibbles(vc[0]) | spread_nibbles(vc[1]) << 4;
-  if (on[0] && on[1]) {
-    *vw = bits;
-  } else {
-    const uint32_t mask = on[0] ? 0x0F0F0F0Fu : 0xF0F0F0F0u;
-    const uint32_t flip = (*reinterpret_cast<volatile uint32_t*>(vw) ^ bits) & mask;
-    if (flip) atomicXor(vw, flip);
+    uint32_t kc[2], vc[2], ksc[2], vsc[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      kc[e] = kv4_quantise(kx[e], &ksc[e]);
+      vc[e] = kv4_quantise(vx[e], &vsc[e]);
+    }
+    if (even < 0 || even > 0x7FFFFFFEll || (!on[0] && !on[1])) continue;
+    const int tile = (int)even >> 4, at = kv4_page_of_tile(M, tile), page = kv4_page(M, b, at);
+    if (page < 0) continue;
+    unsigned char* T = kv4_tile(M, page, h, tile - at * M.tpp);
+    const int slot = (int)even & 15;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (!on[e]) continue;
+      *reinterpret_cast<uint16_t*>(T + (slot + e) * (M.d / 2) + (lane8 >> 1) * (ng * 4) + w * 4 + (lane8 & 1) * 2) =
+          (uint16_t)kc[e];
+      if (lane8 == 0) {
+        uint16_t* sc = reinterpret_cast<uint16_t*>(T + 16 * M.d) + (slot + e) * ng + w;
+        sc[0] = (uint16_t)ksc[e];
+        sc[16 * ng] = (uint16_t)vsc[e];
+      }
+    }
+    uint32_t* vw = reinterpret_cast<uint32_t*>(T + 8 * M.d + (slot >> 1) * M.d + lane8 * (ng * 4) + w * 4);
+    const uint32_t bits = spread_nibbles(vc[0]) | spread_nibbles(vc[1]) << 4;
+    if (on[0] && on[1]) {
+      *vw = bits;
+    } else {
+      const uint32_t mask = on[0] ? 0x0F0F0F0Fu : 0xF0F0F0F0u;
+      const uint32_t flip = (*reinterpret_cast<volatile uint32_t*>(vw) ^ bits) & mask;
+      if (flip) atomicXor(vw, flip);
+    }
   }
 }
 
@@ -160,54 +175,74 @@ __device__ __forceinline__ void store4(void* base, long long at, int dtype, floa
   }
 }
 
-__device__ __forceinline__ float4 codes_to_float4(uint32_t c, float s) {
+// Eight channels: their codes times s, rounded once to the type.
+__device__ __forceinline__ void store8_held(void* base, long long at, int dtype, uint32_t codes, float s) {
   uint32_t h[4];
-  e2m1_to_half2x4(c, h);
-  const float2 lo = unpack_half2(h[0]), hi = unpack_half2(h[1]);
-  return make_float4(lo.x * s, lo.y * s, hi.x * s, hi.y * s);
-}
-
-__global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ Kv4Rows P) {
-  const Kv4Map& M = P.map;
-  const int chunks = M.nkv * M.d / 4, ng = M.d / kKvGroup;
-  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int chunk = (int)(id % chunks);
-  const long long rest = id / chunks;
-  const int pair = (int)(rest % P.npairs);
-  const long long bl = rest / P.npairs;
-  if (bl >= P.B) return;
-  const int b = (int)bl, even = 2 * pair;
-  const int n = P.len ? min(max(__ldg(P.len + b), 0), P.M) : P.M;
-  const int page = even < n ? kv4_page(M, b, even / M.page_size) : -1;
-  float4 k[2], v[2];
+  e2m1_to_half2x4(codes, h);
+  float2 f[4];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) k[e] = v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (page >= 0) {
-    const int in_page = even % M.page_size, slot = in_page & 15;
-    const int h = chunk / (M.d / 4), c4 = chunk - h * (M.d / 4), w = c4 >> 3, lane8 = c4 & 7;
-    const unsigned char* tile = kv4_tile(M, page, h, in_page >> 4);
-    const uint32_t vw = *reinterpret_cast<const uint32_t*>(tile + 8 * M.d + (slot >> 1) * M.d + lane8 * (ng * 4) + w * 4);
+  for (int i = 0; i < 4; ++i) {
+    f[i] = unpack_half2(h[i]);
+    f[i] = make_float2(f[i].x * s, f[i].y * s);
+  }
+  if (dtype == kF32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+    p[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    p[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+    return;
+  }
+  uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (even + e >= n) continue;
-      const uint32_t kc = *reinterpret_cast<const uint16_t*>(tile + (slot + e) * (M.d / 2) + (lane8 >> 1) * (ng * 4) + w * 4 +
-                                                              (lane8 & 1) * 2);
-      const uint16_t* sc = reinterpret_cast<const uint16_t*>(tile + 16 * M.d) + (slot + e) * ng + w;
-      k[e] = codes_to_float4(kc, bf16_bits_f32(sc[0]));
-      // this token's nibbles of the pair's four bytes, packed to 16 bits
-      uint32_t c = (vw >> (4 * e)) & 0x0F0F0F0Fu;
-      c = (c | c >> 4) & 0x00FF00FFu;
-      c = (c | c >> 8) & 0xFFFFu;
-      v[e] = codes_to_float4(c, bf16_bits_f32(sc[16 * ng]));
+  for (int i = 0; i < 4; ++i) {
+    if (dtype == kBF16) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(f[i].x, f[i].y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&a);
+    } else {
+      w[i] = pack_half2(f[i].x, f[i].y);
     }
   }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One thread per (sequence, pair of token slots, 8 channels of a head): one
+// word of key codes per token, two words of value codes for both.
+__global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ Kv4Rows P) {
+  const Kv4Map& M = P.map;
+  const int ng = M.d / kKvGroup;
+  const unsigned id = blockIdx.x * 256u + threadIdx.x, pair = id / (unsigned)P.chunks, chunk = id - pair * P.chunks;
+  if (pair >= (unsigned)P.npairs) return;
+  const int h = chunk / (M.d / 8), c8 = chunk - h * (M.d / 8), w = c8 >> 2, t = c8 & 3;
+  const int even = 2 * (int)pair, tile = even >> 4, at = kv4_page_of_tile(M, tile), slot = even & 15;
   const long long width = (long long)M.nkv * M.d;
+  for (int b = blockIdx.y; b < P.B; b += gridDim.y) {
+    const int n = P.len ? min(max(__ldg(P.len + b), 0), P.M) : P.M;
+    const int page = even < n ? kv4_page(M, b, at) : -1;
+    uint32_t kc[2] = {0u, 0u}, vc[2] = {0u, 0u}, ks[2] = {0u, 0u}, vs[2] = {0u, 0u};
+    if (page >= 0) {
+      const unsigned char* T = kv4_tile(M, page, h, tile - at * M.tpp);
+      const unsigned char* vp = T + 8 * M.d + (slot >> 1) * M.d + 2 * t * (ng * 4) + w * 4;
+      const uint32_t v0 = *reinterpret_cast<const uint32_t*>(vp), v1 = *reinterpret_cast<const uint32_t*>(vp + ng * 4);
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    if (even + e >= P.M) continue;
-    const long long at = ((long long)b * P.M + even + e) * width + 4 * chunk;
-    store4(P.ko, at, P.dtype, k[e]);
-    store4(P.vo, at, P.dtype, v[e]);
+      for (int e = 0; e < 2; ++e) {
+        if (even + e >= n) continue;
+        kc[e] = *reinterpret_cast<const uint32_t*>(T + (slot + e) * (M.d / 2) + t * (ng * 4) + w * 4);
+        const uint16_t* sc = reinterpret_cast<const uint16_t*>(T + 16 * M.d) + (slot + e) * ng + w;
+        ks[e] = sc[0];
+        vs[e] = sc[16 * ng];
+        // this token's nibbles of the eight bytes, packed to 32 bits
+        uint32_t a = (v0 >> (4 * e)) & 0x0F0F0F0Fu, c = (v1 >> (4 * e)) & 0x0F0F0F0Fu;
+        a = (a | a >> 4) & 0x00FF00FFu;
+        c = (c | c >> 4) & 0x00FF00FFu;
+        vc[e] = __byte_perm(a, c, 0x6420);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (even + e >= P.M) continue;
+      const long long o = ((long long)b * P.M + even + e) * width + 8 * chunk;
+      store8_held(P.ko, o, P.dtype, kc[e], bf16_bits_f32(ks[e]));
+      store8_held(P.vo, o, P.dtype, vc[e], bf16_bits_f32(vs[e]));
+    }
   }
 }
 
@@ -216,9 +251,12 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ K
 // values, one pass with a running maximum and sum.  A CTA takes one KV head
 // of one sequence and up to 8 NT of its query rows (rows of the window x the
 // query heads that share the KV head); its warps take pairs of 16-token tiles
-// in turn, and the CTAs of a cluster split the sequence and join through
-// distributed shared memory (no workspace, no atomics: results do not depend
-// on the order of arrival).
+// in turn.  Where that leaves SMs idle several CTAs split a sequence, write
+// their shares to the caller's workspace, and a second kernel joins them in
+// order (no atomics: results do not depend on the order of arrival; nothing in
+// the workspace outlives the call).  Joining through the shared memory of a
+// cluster was slower: a cluster of 16 packs two CTAs on an SM and left half of
+// the SMs idle (one row over 8 heads x 32768 tokens: 23.7 us).
 //
 // Per pair of tiles a warp forms S^T = K q^T with the 16 tokens of a tile as
 // the M operand, straight from the codes, and 8 query rows as N.  The group's
@@ -250,13 +288,17 @@ struct Kv4Attn {
   const int* n_rows;
   const unsigned long long* mask;
   long long qs, os;
-  float scale_log2e;
+  float scale_log2e;      // its magnitude; the sign goes to q
   int M, nq, grp, row_tiles, splits, dtype;
-  int ring_at, ring_stride, res_at;
-  bool qvec;
+  int ring_at, ring_stride, stages;
+  float* part;  // shares of the splits: [unit][split] of m[C], l[C], O[C][D]
+  bool qvec, ovec, negative;
 };
 
-__host__ __device__ constexpr int kv4_stages(int NG) { return NG == 2 ? 4 : 2; }
+constexpr int kKvMaxSplits = 64;
+constexpr int kKvMaxWarps = 8;
+// CTAs of 8 warps that share an SM, by the registers of the accumulators.
+__host__ __device__ constexpr int kv4_ctas(int NG, int NT) { return NT * NG <= 4 ? 2 : 1; }
 
 template <int N>
 __device__ __forceinline__ void lds_words(const unsigned char* p, uint32_t (&w)[N]) {
@@ -285,93 +327,145 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float pow2_of_biased(int e) { return __uint_as_float((uint32_t)e << 23); }
+
+// Factor of a share whose reference is m in a sum whose reference is top.
+__device__ __forceinline__ float share_factor(float m, float top) {
+  return m == -INFINITY && top == -INFINITY ? 0.0f : (m == top ? 1.0f : ex2(m - top));
+}
+
+// Four channels of query row rr (of those that share KV head h): v over the
+// sum s whose reference is m (log2 units), and the log-sum-exp.
+template <int D>
+__device__ __forceinline__ void kv4_write(const Kv4Attn& P, int b, int h, int rr, int ch, float m, float s, float4 v) {
+  const int row = rr / P.grp, e = rr - row * P.grp;
+  if (s == 0.0f) {
+    v = make_float4(0.f, 0.f, 0.f, 0.f);  // a row that sees nothing
+  } else {
+    const float inv = __frcp_rn(s);
+    v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  }
+  const long long at = ((long long)b * P.M + row) * P.os + (long long)(h * P.grp + e) * D + ch;
+  if (P.ovec) {
+    store4(P.o, at, P.dtype, v);
+  } else {
+    store_elem(P.o, at, P.dtype, v.x);
+    store_elem(P.o, at + 1, P.dtype, v.y);
+    store_elem(P.o, at + 2, P.dtype, v.z);
+    store_elem(P.o, at + 3, P.dtype, v.w);
+  }
+  if (ch == 0 && P.lse)
+    P.lse[((long long)b * P.M + row) * P.nq + h * P.grp + e] =
+        s == 0.0f ? -INFINITY : (m + log2f(s)) * 0.69314718055994530942f;
+}
 
 template <int NG, int NT, int QT, int PT>
-__global__ void __launch_bounds__(256, (NT * NG <= 8 && NG <= 4) ? 2 : 1) kv4_attention_kernel(const __grid_constant__ Kv4Attn P) {
-  constexpr int D = 32 * NG, TB = 18 * D, CH = TB / 16, ST = kv4_stages(NG), C = 8 * NT, QS = 2 * D + 64, RS = D + 8;
+__global__ void __launch_bounds__(32 * kKvMaxWarps, kv4_ctas(NG, NT)) kv4_attention_kernel(const __grid_constant__ Kv4Attn P) {
+  constexpr int D = 32 * NG, TB = 18 * D, CH = TB / 16, C = 8 * NT, QS = 2 * D + 64, RS = D + 8;
+  constexpr int E0 = 27;                   // biased exponent that the scales of the values start from (2^-100)
   constexpr bool QREG = NG * NT * QT <= 4;  // q operands kept in registers
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ float s_fac[C];
   __shared__ int s_row[C];
   __shared__ unsigned long long s_mask[C];
-  __shared__ float s_ml[2 * C];
-  namespace cg = cooperative_groups;
+  __shared__ float s_m[C], s_l[C];                              // this CTA's references and sums
+  __shared__ float s_pm[kKvMaxWarps][C], s_pl[kKvMaxWarps][C];  // the warps'; s_pm becomes their factors
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the kernel that joins the splits, where there is one)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3, W = blockDim.x >> 5;
   const Kv4Map& M = P.map;
   const int unit = blockIdx.x / P.splits, sp = blockIdx.x - unit * P.splits;
   const int rt = unit % P.row_tiles, bh = unit / P.row_tiles, h = bh % M.nkv, b = bh / M.nkv;
   const int nr = P.n_rows ? min(max(__ldg(P.n_rows + b), 0), P.M) : P.M;
   const int ncol = min(C, nr * P.grp - rt * C);
-  if (ncol <= 0) return;  // the same for every CTA of the cluster
+  if (ncol <= 0) return;
   const int len = min(max(__ldg(P.kv_len + b), 0), M.max_pages * M.page_size);
   const int base = len - nr;  // position of the window's row 0
-  const int tiles = (len + 15) >> 4;
-  const int ta = (int)((long long)tiles * sp / P.splits), te = (int)((long long)tiles * (sp + 1) / P.splits);
-  const int own = te - ta - 2 * warp;
-  const int nit = own > 0 ? (own + 2 * W - 1) / (2 * W) : 0;
+  // Pairs of tiles go round the warps of all splits in turn: which a warp takes
+  // does not depend on the length, so its first pages are known before it is.
+  const int tiles = (len + 15) >> 4, all_warps = W * P.splits, me = sp * W + warp;
+  const int pairs = (tiles + 1) >> 1, nit = pairs > me ? (pairs - me + all_warps - 1) / all_warps : 0;
   unsigned char* ring = sm + P.ring_at + (size_t)warp * P.ring_stride;
+  const unsigned char* head = M.cache + (long long)h * M.tpp * TB + lane * 16;
 
   uint32_t okbits = 0;  // tiles of the ring that hold tokens: bit 2 * stage + sub
-  auto issue = [&](int i) {
+  int page[2], in[2];   // pages of the pair that is copied next, and the tiles' places in them
+  auto look = [&](int i) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int j = 2 * (me + all_warps * i) + u, at = kv4_page_of_tile(M, j);
+      in[u] = j - at * M.tpp;
+      page[u] = kv4_page(M, b, at);
+    }
+  };
+  auto issue = [&](int i, int stage) {
     if (i < nit) {
-      const int j0 = ta + 2 * (warp + W * i), stage = i % ST;
-      const unsigned char* src[2];
+      unsigned char* dst = ring + stage * (2 * TB) + lane * 16;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        src[u] = nullptr;
-        if (j0 + u < te) {
-          const int p0 = (j0 + u) * 16, at = p0 / M.page_size, page = kv4_page(M, b, at);
-          if (page >= 0) src[u] = kv4_tile(M, page, h, (p0 - at * M.page_size) >> 4);
-        }
         const uint32_t bit = 1u << (2 * stage + u);
-        okbits = src[u] ? okbits | bit : okbits & ~bit;
-      }
-      unsigned char* dst = ring + stage * (2 * TB);
+        if (page[u] >= 0 && 2 * (me + all_warps * i) + u < tiles) {
+          okbits |= bit;
+          const unsigned char* src = head + page[u] * M.page_stride + in[u] * TB;
 #pragma unroll
-      for (int c0 = 0; c0 < 2 * CH; c0 += 32) {
-        const int c = c0 + lane;
-        if (c < 2 * CH) {
-          const unsigned char* s = c < CH ? src[0] : src[1];
-          if (s) cp_async16(dst + c * 16, s + (c < CH ? c : c - CH) * 16);
+          for (int r = 0; r < (CH + 31) / 32; ++r)
+            if (32 * r + 32 <= CH || lane < CH - 32 * r) cp_async16(dst + u * TB + r * 512, src + r * 512);
+        } else {
+          okbits &= ~bit;
         }
       }
+      look(i + 1);
     }
     cp_async_commit();
   };
-#pragma unroll
-  for (int i = 0; i < ST - 1; ++i) issue(i);
+  look(0);
+  const int ST = P.stages;
+#pragma unroll 1
+  for (int i = 0; i < ST - 1; ++i) issue(i, i);
 
-  // query rows: one warp per row; a column past the rows holds zeros
-  for (int c = warp; c < C; c += W) {
-    const int rr = rt * C + c, m = rr / P.grp, e = rr - m * P.grp;
-    const bool in = c < ncol;
-    const long long at = ((long long)b * P.M + m) * P.qs + (long long)(h * P.grp + e) * D;
-    float4 v[(D + 127) / 128];
-    uint32_t mx = 0;
+  // query rows: one warp per row, several loads in flight; a column past the rows holds zeros
+  constexpr int QU = 4, QC = (D + 127) / 128;
+  for (int c0 = warp; c0 < C; c0 += QU * W) {
+    float4 v[QU][QC];
 #pragma unroll
-    for (int i = 0; i < (D + 127) / 128; ++i) {
-      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int k = i * 128 + lane * 4;
-      if (in && k < D) v[i] = load4(static_cast<const unsigned char*>(P.q) + at * elem_bytes(P.dtype), P.dtype, k, D, P.qvec);
-      mx = max(mx, max(max(finite_abs_bits(v[i].x), finite_abs_bits(v[i].y)),
-                       max(finite_abs_bits(v[i].z), finite_abs_bits(v[i].w))));
-    }
-    float up, down;
-    pow2_normaliser(__reduce_max_sync(0xffffffffu, mx), &up, &down);
+    for (int k = 0; k < QU; ++k) {
+      const int c = c0 + k * W, rr = rt * C + c, m = rr / P.grp, e = rr - m * P.grp;
+      const long long at = ((long long)b * P.M + m) * P.qs + (long long)(h * P.grp + e) * D;
 #pragma unroll
-    for (int i = 0; i < (D + 127) / 128; ++i) {
-      const int k = i * 128 + lane * 4;
-      if (k >= D) continue;
-      const float x0 = v[i].x * up, x1 = v[i].y * up, x2 = v[i].z * up, x3 = v[i].w * up;
-      *reinterpret_cast<uint2*>(sm + c * QS + k * 2) = make_uint2(pack_half2(x0, x1), pack_half2(x2, x3));
-      if (QT == 2)
-        *reinterpret_cast<uint2*>(sm + (C + c) * QS + k * 2) =
-            make_uint2(pack_half2(fp16_rest(x0), fp16_rest(x1)), pack_half2(fp16_rest(x2), fp16_rest(x3)));
+      for (int i = 0; i < QC; ++i) {
+        v[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int x = i * 128 + lane * 4;
+        if (c < ncol && x < D)
+          v[k][i] = load4(static_cast<const unsigned char*>(P.q) + at * elem_bytes(P.dtype), P.dtype, x, D, P.qvec);
+      }
     }
-    if (lane == 0) {
-      s_fac[c] = down * P.scale_log2e;
-      s_row[c] = m;
-      s_mask[c] = in && P.mask ? P.mask[(long long)b * P.M + m] : ~0ull;
+#pragma unroll
+    for (int k = 0; k < QU; ++k) {
+      const int c = c0 + k * W;
+      if (c >= C) break;
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < QC; ++i)
+        mx = max(mx, max(max(finite_abs_bits(v[k][i].x), finite_abs_bits(v[k][i].y)),
+                         max(finite_abs_bits(v[k][i].z), finite_abs_bits(v[k][i].w))));
+      float up, down;
+      pow2_normaliser(__reduce_max_sync(0xffffffffu, mx), &up, &down);
+      if (P.negative) up = -up;
+#pragma unroll
+      for (int i = 0; i < QC; ++i) {
+        const int x = i * 128 + lane * 4;
+        if (x >= D) continue;
+        const float x0 = v[k][i].x * up, x1 = v[k][i].y * up, x2 = v[k][i].z * up, x3 = v[k][i].w * up;
+        *reinterpret_cast<uint2*>(sm + c * QS + x * 2) = make_uint2(pack_half2(x0, x1), pack_half2(x2, x3));
+        if (QT == 2)
+          *reinterpret_cast<uint2*>(sm + (C + c) * QS + x * 2) =
+              make_uint2(pack_half2(fp16_rest(x0), fp16_rest(x1)), pack_half2(fp16_rest(x2), fp16_rest(x3)));
+      }
+      if (lane == 0) {
+        const int m = (rt * C + c) / P.grp;
+        s_fac[c] = fmaxf(down * P.scale_log2e, 1e-37f);  // never zero: -infinity times it stays -infinity
+        s_row[c] = m;
+        s_mask[c] = c < ncol && P.mask ? P.mask[(long long)b * P.M + m] : ~0ull;
+      }
     }
   }
   __syncthreads();
@@ -393,11 +487,15 @@ __global__ void __launch_bounds__(256, (NT * NG <= 8 && NG <= 4) ? 2 : 1) kv4_at
           qr[(w * NT + n) * QT + x] = *reinterpret_cast<const uint4*>(qcol + (x * C + n * 8) * QS + w * 64);
   }
 
-  float O[NG][2][NT][4], mref[NT][2], l[NT][2];
+  // Per column: the reference m (log2 units), the score above which it moves
+  // (in raw score units), and what is taken from a score: m less the power of
+  // two that brings the values' scales to [2^6, 2^7), so that it costs nothing
+  // to apply.  l and O carry that power; it is taken out at the end.
+  float O[NG][2][NT][4], mref[NT][2], thr[NT][2], sub[NT][2], l[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) { mref[n][c] = -INFINITY; l[n][c] = 0.0f; }
+    for (int c = 0; c < 2; ++c) { mref[n][c] = thr[n][c] = -INFINITY; l[n][c] = sub[n][c] = 0.0f; }
 #pragma unroll
     for (int w = 0; w < NG; ++w)
 #pragma unroll
@@ -405,21 +503,24 @@ __global__ void __launch_bounds__(256, (NT * NG <= 8 && NG <= 4) ? 2 : 1) kv4_at
 #pragma unroll
         for (int c = 0; c < 4; ++c) O[w][u][n][c] = 0.0f;
   }
-  int ecur = 7;  // biased exponent of the largest value scale seen
-  float en = __uint_as_float((uint32_t)(127 + 6 + 127 - 7) << 23);  // 2^(6 - (ecur - 127))
+  uint32_t ecur = E0;  // biased exponent of the largest value scale seen
 
+  int stage = 0;
+#pragma unroll 1
   for (int i = 0; i < nit; ++i) {
     __syncwarp();  // every lane is done with the stage that is filled next
-    issue(i + ST - 1);
-    cp_async_wait_group<ST - 1>();
+    issue(i + ST - 1, stage == 0 ? ST - 1 : stage - 1);
+    if (ST == 2) cp_async_wait_group<1>();
+    else cp_async_wait_group<3>();
     __syncwarp();
-    const int stage = i % ST, p0 = (ta + 2 * (warp + W * i)) * 16;
+    const int p0 = 32 * (me + all_warps * i);
     const unsigned char* st = ring + stage * (2 * TB);
     const uint32_t ok = (okbits >> (2 * stage)) & 3u;
+    stage = stage + 1 == ST ? 0 : stage + 1;
     const bool edge = ok != 3u || p0 + 31 >= base;  // some token is not seen by every row
 
     float sc[2][NT][4];
-    uint32_t vs[2][2][NG / 2], keep[2][2][NT];
+    uint32_t vs[2][2][NG / 2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const unsigned char* T = st + s * TB;
@@ -430,10 +531,6 @@ __global__ void __launch_bounds__(256, (NT * NG <= 8 && NG <= 4) ? 2 : 1) kv4_at
       lds_words<NG / 2>(T + 16 * D + (g + 8) * (NG * 2), sb);
       lds_words<NG / 2>(T + 17 * D + g * (NG * 2), vs[s][0]);
       lds_words<NG / 2>(T + 17 * D + (g + 8) * (NG * 2), vs[s][1]);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sc[s][n][c] = 0.0f;
 #pragma unroll
       for (int w = 0; w < NG; ++w) {
         uint32_t a[4], c4[4];
@@ -450,17 +547,9 @@ __global__ void __launch_bounds__(256, (NT * NG <= 8 && NG <= 4) ? 2 : 1) kv4_at
             mma_f16_16816(acc, a[0], c4[0], a[1], c4[1], q4.x, q4.y);
             mma_f16_16816(acc, a[2], c4[2], a[3], c4[3], q4.z, q4.w);
           }
-          sc[s][n][0] = fmaf(f0, acc[0], sc[s][n][0]);
-          sc[s][n][1] = fmaf(f0, acc[1], sc[s][n][1]);
-          sc[s][n][2] = fmaf(f1, acc[2], sc[s][n][2]);
-          sc[s][n][3] = fmaf(f1, acc[3], sc[s][n][3]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sc[s][n][c] = w == 0 ? (c < 2 ? f0 : f1) * acc[c] : fmaf(c < 2 ? f0 : f1, acc[c], sc[s][n][c]);
         }
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sc[s][n][c] *= fac[n][c & 1];
-        keep[s][0][n] = keep[s][1][n] = 0xFFFFFFFFu;
       }
       if (edge) {
 #pragma unroll
@@ -476,10 +565,7 @@ __global__ void __launch_bounds__(256, (NT * NG <= 8 && NG <= 4) ? 2 : 1) kv4_at
             for (int c = 0; c < 2; ++c) {
               const int col = n * 8 + 2 * t + c;
               const bool see = there && (j < 0 || (P.mask ? (s_mask[col] >> j) & 1ull : (unsigned long long)(j <= s_row[col])));
-              if (!see) {
-                sc[s][n][2 * hh + c] = -INFINITY;
-                keep[s][hh][n] &= c ? 0x0000FFFFu : 0xFFFF0000u;  // a masked token adds nothing, whatever its scale is
-              }
+              if (!see) sc[s][n][2 * hh + c] = -INFINITY;
             }
         }
       }
@@ -491,14 +577,14 @@ __global__ void __launch_bounds__(256, (NT * NG <= 8 && NG <= 4) ? 2 : 1) kv4_at
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) move |= sc[s][n][c] > mref[n][c & 1] + 8.0f;
-#pragma unroll
       for (int w = 0; w < NG / 2; ++w) top2 = __vmaxu2(top2, __vmaxu2(vs[s][0][w], vs[s][1][w]));
     }
-    const int etop = (int)(max(top2 & 0xFFFFu, top2 >> 16) >> 7);
-    if (__any_sync(0xffffffffu, move || etop > ecur)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        move |= fmaxf(fmaxf(fmaxf(sc[0][n][c], sc[0][n][2 + c]), sc[1][n][c]), sc[1][n][2 + c]) > thr[n][c];
+    if (__any_sync(0xffffffffu, move || (max(top2 & 0xFFFFu, top2 >> 16) >> 7) > ecur)) {
       uint32_t e = 0;  // the largest exponent of a finite scale
 #pragma unroll
       for (int s = 0; s < 2; ++s)
@@ -509,103 +595,121 @@ __global__ void __launch_bounds__(256, (NT * NG <= 8 && NG <= 4) ? 2 : 1) kv4_at
             const uint32_t x = (vs[s][hh][w >> 1] >> (16 * (w & 1)) & 0xFFFFu) >> 7;
             if (x < 255u) e = max(e, x);
           }
-      const int enew = max(ecur, (int)__reduce_max_sync(0xffffffffu, e));
-      const float er = __uint_as_float((uint32_t)max(127 + ecur - enew, 0) << 23);
+      const uint32_t enew = max(ecur, __reduce_max_sync(0xffffffffu, e));
+      const float er = pow2_of_biased(max(127 + (int)ecur - (int)enew, 0));
       ecur = enew;
-      en = __uint_as_float((uint32_t)(127 + 6 + 127 - ecur) << 23);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float mx = fmaxf(fmaxf(sc[0][n][c], sc[0][n][2 + c]), fmaxf(sc[1][n][c], sc[1][n][2 + c]));
+          float mx = fmaxf(fmaxf(sc[0][n][c], sc[0][n][2 + c]), fmaxf(sc[1][n][c], sc[1][n][2 + c])) * fac[n][c];
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
           mx = fmaxf(mx, mref[n][c]);
-          const float al = mx == mref[n][c] ? 1.0f : ex2(mref[n][c] - mx);
+          const float al = (mx == mref[n][c] ? 1.0f : ex2(mref[n][c] - mx)) * er;
           mref[n][c] = mx;
+          thr[n][c] = __fdiv_rn(mx + 8.0f, fac[n][c]);
+          sub[n][c] = mx == -INFINITY ? 0.0f : mx - (float)(6 + 127 - (int)ecur);
           l[n][c] *= al;
 #pragma unroll
           for (int w = 0; w < NG; ++w)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              O[w][u][n][c] *= al * er;
-              O[w][u][n][2 + c] *= al * er;
+              O[w][u][n][c] *= al;
+              O[w][u][n][2 + c] *= al;
             }
         }
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float ref = mref[n][c] == -INFINITY ? 0.0f : mref[n][c];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const float pa = ex2(sc[s][n][c] - ref), pb = ex2(sc[s][n][2 + c] - ref);
-          l[n][c] += pa + pb;
-          sc[s][n][c] = pa;
-          sc[s][n][2 + c] = pb;
-        }
-      }
-
-    // O^T += V^T P^T
-    uint32_t va[2][NG], vb[2][NG];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      lds_words<NG>(st + s * TB + 8 * D + t * D + g * (NG * 4), va[s]);
-      lds_words<NG>(st + s * TB + 8 * D + (t + 4) * D + g * (NG * 4), vb[s]);
-    }
-#pragma unroll
-    for (int w = 0; w < NG; ++w) {
-      uint32_t B[2][NT][PT][2];
-#pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const float f = scale_of(vs[s][hh], w) * en;
+        for (int c = 0; c < 4; ++c) {
+          sc[s][n][c] = ex2(fmaf(sc[s][n][c], fac[n][c & 1], -sub[n][c & 1]));
+          l[n][c & 1] += sc[s][n][c];
+        }
+
+    // O^T += V^T P^T.  KEEP: some weights are masked, and a masked token adds
+    // nothing whatever its scale is.
+    auto values = [&](auto keep_tag) {
+      constexpr bool KEEP = decltype(keep_tag)::value;
+      uint32_t keep[2][2][NT];
+      if constexpr (KEEP) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const float x = sc[s][n][2 * hh] * f, y = sc[s][n][2 * hh + 1] * f;
-            const uint32_t hi = pack_half2(x, y) & keep[s][hh][n];
-            B[s][n][0][hh] = movmatrix_trans(hi);
-            if (PT == 2) {
-              const float2 r = unpack_half2(hi);
-              B[s][n][PT - 1][hh] = movmatrix_trans(pack_half2(x - r.x, y - r.y) & keep[s][hh][n]);
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+              keep[s][hh][n] = (sc[s][n][2 * hh] == 0.0f ? 0u : 0x0000FFFFu) | (sc[s][n][2 * hh + 1] == 0.0f ? 0u : 0xFFFF0000u);
+      }
+      uint32_t va[2][NG], vb[2][NG];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        lds_words<NG>(st + s * TB + 8 * D + t * D + g * (NG * 4), va[s]);
+        lds_words<NG>(st + s * TB + 8 * D + (t + 4) * D + g * (NG * 4), vb[s]);
+      }
+#pragma unroll
+      for (int w = 0; w < NG; ++w) {
+        uint32_t B[2][NT][PT][2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const float f = scale_of(vs[s][hh], w);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const float x = sc[s][n][2 * hh] * f, y = sc[s][n][2 * hh + 1] * f;
+              uint32_t hi = pack_half2(x, y);
+              if constexpr (KEEP) hi &= keep[s][hh][n];
+              B[s][n][0][hh] = movmatrix_trans(hi);
+              if constexpr (PT == 2) {
+                const float2 r = unpack_half2(hi);
+                uint32_t lo = pack_half2(x - r.x, y - r.y);
+                if constexpr (KEEP) lo &= keep[s][hh][n];
+                B[s][n][PT - 1][hh] = movmatrix_trans(lo);
+              }
             }
           }
-        }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float acc[NT][4];
-        if (QT == 2)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+        uint32_t a[2][4], c4[2][4];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          uint32_t a[4], c4[4];
-          e2m1_to_half2x4(va[s][w], a);
-          e2m1_to_half2x4(vb[s][w], c4);
+          e2m1_to_half2x4(va[s][w], a[s]);
+          e2m1_to_half2x4(vb[s][w], c4[s]);
+        }
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+        for (int u = 0; u < 2; ++u) {
+          float acc[NT][4];
+          if constexpr (QT == 2)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int x = PT - 1; x >= 0; --x)
-              mma_f16_16816(QT == 2 ? acc[n] : O[w][u][n], a[2 * u], a[2 * u + 1], c4[2 * u], c4[2 * u + 1], B[s][n][x][0],
-                            B[s][n][x][1]);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma_f16_16816(QT == 2 ? acc[n] : O[w][u][n], a[s][2 * u], a[s][2 * u + 1], c4[s][2 * u], c4[s][2 * u + 1],
+                              B[s][n][x][0], B[s][n][x][1]);
+          if constexpr (QT == 2)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) O[w][u][n][c] += acc[n][c];
         }
-        if (QT == 2)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) O[w][u][n][c] += acc[n][c];
       }
-    }
+    };
+    if (edge) values(std::true_type{});
+    else values(std::false_type{});
   }
   cp_async_wait_group<0>();
   __syncwarp();
 
   // the warps' shares through shared memory (each over its own ring)
   {
-    float* mo = reinterpret_cast<float*>(ring);  // [C][RS], then m[C], l[C]
-    const float back = __uint_as_float((uint32_t)(127 + ecur - 127 - 6) << 23);  // 2^(ecur - 127 - 6)
+    float* mo = reinterpret_cast<float*>(ring);  // [C][RS]
+    const float back = pow2_of_biased((int)ecur - 6);  // 2^(ecur - 127 - 6)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -615,8 +719,8 @@ __global__ void __launch_bounds__(256, (NT * NG <= 8 && NG <= 4) ? 2 : 1) kv4_at
         for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         const int col = n * 8 + 2 * t + c;
         if (g == 0) {
-          mo[C * RS + col] = mref[n][c];
-          mo[C * RS + C + col] = s;
+          s_pm[warp][col] = mref[n][c];
+          s_pl[warp][col] = s * back;
         }
 #pragma unroll
         for (int w = 0; w < NG; ++w)
@@ -627,53 +731,89 @@ __global__ void __launch_bounds__(256, (NT * NG <= 8 && NG <= 4) ? 2 : 1) kv4_at
       }
   }
   __syncthreads();
-  const int stride = P.ring_stride / 4;
-  const float* all = reinterpret_cast<const float*>(sm + P.ring_at);
-  float* res = reinterpret_cast<float*>(sm + P.res_at);
-  const float ln2 = 0.69314718055994530942f;
-  auto write = [&](int col, int ch, float m, float s, float v) {
-    const int rr = rt * C + col, row = rr / P.grp, e = rr - row * P.grp;
-    store_elem(P.o, ((long long)b * P.M + row) * P.os + (long long)(h * P.grp + e) * D + ch, P.dtype, s > 0.0f || s != s ? v / s : 0.0f);
-    if (ch == 0 && P.lse)
-      P.lse[((long long)b * P.M + row) * P.nq + h * P.grp + e] = s == 0.0f ? -INFINITY : (m + log2f(s)) * ln2;
-  };
-  for (int i = tid; i < ncol * D; i += blockDim.x) {
-    const int col = i / D, ch = i - col * D;
-    float m = -INFINITY;
-    for (int k = 0; k < W; ++k) m = fmaxf(m, all[k * stride + C * RS + col]);
-    float s = 0.0f, v = 0.0f;
-    const float ref = m == -INFINITY ? 0.0f : m;
+  // one reference and sum per column; the warps' factors replace their references
+  if (tid < C) {
+    float m = -INFINITY, sum = 0.0f;
+    for (int k = 0; k < W; ++k) m = fmaxf(m, s_pm[k][tid]);
     for (int k = 0; k < W; ++k) {
-      const float* x = all + k * stride;
-      const float mk = x[C * RS + col], f = mk == m && m != -INFINITY ? 1.0f : ex2(mk - ref);
-      s = fmaf(f, x[C * RS + C + col], s);
-      v = fmaf(f, x[col * RS + ch], v);
+      const float f = share_factor(s_pm[k][tid], m);
+      sum = fmaf(f, s_pl[k][tid], sum);
+      s_pm[k][tid] = f;
+    }
+    s_m[tid] = m;
+    s_l[tid] = sum;
+  }
+  __syncthreads();
+  const float* all = reinterpret_cast<const float*>(sm + P.ring_at);
+  float* part = P.splits > 1 ? P.part + (long long)blockIdx.x * (C * (D + 2)) : nullptr;
+  for (int i = tid; i < ncol * (D / 4); i += blockDim.x) {
+    const int col = i / (D / 4), ch = 4 * (i - col * (D / 4));
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kKvMaxWarps; ++k) {
+      if (k >= W) break;
+      const float4 x = *reinterpret_cast<const float4*>(all + k * (P.ring_stride / 4) + col * RS + ch);
+      const float f = s_pm[k][col];
+      v = make_float4(fmaf(f, x.x, v.x), fmaf(f, x.y, v.y), fmaf(f, x.z, v.z), fmaf(f, x.w, v.w));
     }
     if (P.splits == 1) {
-      write(col, ch, m, s, v);
+      kv4_write<D>(P, b, h, rt * C + col, ch, s_m[col], s_l[col], v);
     } else {
-      res[i] = v;
-      if (ch == 0) { s_ml[col] = m; s_ml[C + col] = s; }
+      *reinterpret_cast<float4*>(part + 2 * C + col * D + ch) = v;
+      if (ch == 0) {
+        part[col] = s_m[col];
+        part[C + col] = s_l[col];
+      }
     }
   }
-  if (P.splits == 1) return;
-  // the CTAs of the cluster: each joins a share of the outputs
-  cg::cluster_group cl = cg::this_cluster();
-  cl.sync();
-  for (int i = sp * blockDim.x + tid; i < ncol * D; i += P.splits * blockDim.x) {
-    const int col = i / D, ch = i - col * D;
-    float m = -INFINITY;
-    for (int k = 0; k < P.splits; ++k) m = fmaxf(m, *cl.map_shared_rank(s_ml + col, k));
-    const float ref = m == -INFINITY ? 0.0f : m;
-    float s = 0.0f, v = 0.0f;
-    for (int k = 0; k < P.splits; ++k) {
-      const float mk = *cl.map_shared_rank(s_ml + col, k), f = mk == m && m != -INFINITY ? 1.0f : ex2(mk - ref);
-      s = fmaf(f, *cl.map_shared_rank(s_ml + C + col, k), s);
-      v = fmaf(f, *cl.map_shared_rank(res + i, k), v);
-    }
-    write(col, ch, m, s, v);
+}
+
+// Joins the splits of a sequence: one warp per column, four channels a lane
+// (D / 128 times); the references of all splits first, a lane each.
+template <int NG, int NT>
+__global__ void __launch_bounds__(128) kv4_join_kernel(const __grid_constant__ Kv4Attn P) {
+  constexpr int D = 32 * NG, C = 8 * NT, SIZE = C * (D + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int id = blockIdx.x * 4 + warp, unit = id / C, col = id - unit * C;  // (the grid is units * C / 4 exactly)
+  const int rt = unit % P.row_tiles, bh = unit / P.row_tiles, h = bh % P.map.nkv, b = bh / P.map.nkv;
+  const int nr = P.n_rows ? min(max(__ldg(P.n_rows + b), 0), P.M) : P.M;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (rt * C + col >= nr * P.grp) return;
+  const float* part = P.part + (long long)unit * P.splits * SIZE;
+  float m[kKvMaxSplits / 32], l[kKvMaxSplits / 32], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kKvMaxSplits / 32; ++i) {
+    const int k = i * 32 + lane;
+    m[i] = k < P.splits ? __ldcg(part + (long long)k * SIZE + col) : -INFINITY;
+    l[i] = k < P.splits ? __ldcg(part + (long long)k * SIZE + C + col) : 0.0f;
+    top = fmaxf(top, m[i]);
   }
-  cl.sync();  // no CTA leaves while another reads its shared memory
+  top = warp_max(top);
+#pragma unroll
+  for (int i = 0; i < kKvMaxSplits / 32; ++i) {
+    m[i] = share_factor(m[i], top);
+    sum = fmaf(m[i], l[i], sum);
+  }
+  sum = warp_sum(sum);
+#pragma unroll 1
+  for (int ch = lane * 4; ch < (D < 128 ? 128 : D); ch += 128) {  // (every lane takes part in the shuffles)
+    const float* at = part + 2 * C + col * D + min(ch, D - 4);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k0 = 0; k0 < P.splits; k0 += 8) {
+      float4 x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < P.splits) x[k] = __ldcg(reinterpret_cast<const float4*>(at + (long long)(k0 + k) * SIZE));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float f = __shfl_sync(0xffffffffu, k0 >= 32 ? m[1] : m[0], (k0 + k) & 31);
+        if (k0 + k < P.splits)
+          v = make_float4(fmaf(f, x[k].x, v.x), fmaf(f, x[k].y, v.y), fmaf(f, x[k].z, v.z), fmaf(f, x[k].w, v.w));
+      }
+    }
+    if (ch < D) kv4_write<D>(P, b, h, rt * C + col, ch, top, sum, v);
+  }
 }
 
 }  // namespace cpk
@@ -696,7 +836,17 @@ static Kv4Map kv4_map(const Kv4Shape& S, void* cache, const int* pages, int max_
   M.n_pages = S.n_pages;
   M.nkv = S.nkv;
   M.d = S.d;
+  M.tpp = S.page_size / 16;
+  M.tpp_shift = -1;
+  for (int i = 0; i < 20; ++i)
+    if (M.tpp == 1 << i) M.tpp_shift = i;
+  M.page_stride = (long long)S.nkv * M.tpp * kv4_tile_bytes(S.d);
   return M;
+}
+
+// One thread per pair of slots and chunk of a sequence; sequences past the grid's second axis by a loop.
+static dim3 rows_grid(const Kv4Rows& P) {
+  return dim3((unsigned)(((long long)P.npairs * P.chunks + 255) / 256), std::min(P.B, 65535));
 }
 
 cudaError_t launch_kv4_append(const Kv4Shape& S, void* cache, const int* pages, int max_pages, int B, int M, const int* pos,
@@ -708,11 +858,10 @@ cudaError_t launch_kv4_append(const Kv4Shape& S, void* cache, const int* pages, 
   P.pos = pos; P.len = len;
   P.B = B; P.M = M; P.dtype = dtype;
   P.npairs = M / 2 + 1;
-  const int es = elem_bytes(dtype);
-  P.kvec = ks * es % (4 * es) == 0;
-  P.vvec = vs * es % (4 * es) == 0;
-  const long long threads = (long long)B * P.npairs * (S.nkv * S.d / 4);
-  kv4_append_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(P);
+  P.chunks = S.nkv * S.d / 4;
+  P.kvec = ks % 4 == 0;
+  P.vvec = vs % 4 == 0;
+  kv4_append_kernel<<<rows_grid(P), 256, 0, s>>>(P);
   return cudaGetLastError();
 }
 
@@ -724,49 +873,87 @@ cudaError_t launch_kv4_read(const Kv4Shape& S, const void* cache, const int* pag
   P.len = len;
   P.B = B; P.M = T; P.dtype = dtype;
   P.npairs = (T + 1) / 2;
-  const long long threads = (long long)B * P.npairs * (S.nkv * S.d / 4);
-  kv4_read_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(P);
+  P.chunks = S.nkv * S.d / 8;
+  kv4_read_kernel<<<rows_grid(P), 256, 0, s>>>(P);
   return cudaGetLastError();
 }
 
+// How a call is laid out: query rows per CTA (8 NT), warps of a CTA, and CTAs
+// that split a sequence.
+struct Kv4Plan {
+  int NT, W, row_tiles, splits;
+  long long units;
+  size_t work;  // bytes of the shares
+};
+
+static Kv4Plan kv4_plan(const Kv4Shape& S, int max_pages, int B, int M, int nq, int dtype, int sms) {
+  Kv4Plan L;
+  const int NG = S.d / 32, rows = M * (nq / S.nkv), tiles = max_pages * (S.page_size / 16);
+  // the MMA's 8 columns, or 16; 32 only at 128 channels and 16-bit types (64
+  // rows x 4 over 4096 tokens: 205 against 218 us), not at 64 channels, where
+  // two CTAs of 16 columns share an SM (111 against 128 us), nor where the
+  // accumulators spill
+  const int most = NG == 4 && dtype != kF32 ? 4 : 2;
+  L.NT = std::min(rows <= 8 ? 1 : (rows <= 16 ? 2 : 4), most);
+  L.row_tiles = (rows + 8 * L.NT - 1) / (8 * L.NT);
+  L.units = (long long)B * S.nkv * L.row_tiles;
+  // warps: two tiles each at least, but four for the rows of q and the outputs
+  L.W = 4;
+  while (L.W < kKvMaxWarps && 4 * L.W <= tiles) L.W *= 2;
+  // CTAs of a sequence: as many as the SMs hold at once, while every warp
+  // keeps four tiles
+  const long long slots = (long long)sms * kv4_ctas(NG, L.NT);
+  L.splits = (int)std::max<long long>(1, std::min<long long>(std::min<long long>(slots / std::max(L.units, 1ll), kKvMaxSplits),
+                                                             tiles / (4 * L.W)));
+  L.work = L.splits > 1 ? (size_t)L.units * L.splits * (8 * L.NT) * (S.d + 2) * 4 : 0;
+  return L;
+}
+
+size_t kv4_attention_work(const Kv4Shape& S, int max_pages, int B, int M, int nq, int dtype, int sms) {
+  return kv4_plan(S, max_pages, B, M, nq, dtype, sms).work;
+}
+
 template <int NG, int NT, int QT, int PT>
-static cudaError_t launch_attention(Kv4Attn& P, int W, long long units, cudaStream_t s) {
+static cudaError_t launch_attention(Kv4Attn& P, const Kv4Plan& L, int sms, cudaStream_t s) {
   constexpr int D = 32 * NG, C = 8 * NT;
-  const size_t merge = (size_t)(C * (D + 8) + 2 * C) * 4, ring = (size_t)kv4_stages(NG) * 2 * kv4_tile_bytes(D);
+  // Pairs of tiles in the ring of a warp: two, four where one CTA has the SM
+  // to itself or the pairs are small, so that enough bytes are on their way.
+  P.stages = NG == 2 || (NG == 4 && L.units * P.splits <= sms) ? 4 : 2;
+  const size_t merge = (size_t)C * (D + 8) * 4, ring = (size_t)P.stages * 2 * kv4_tile_bytes(D);
   P.ring_at = (C * QT * (2 * D + 64) + 127) / 128 * 128;
   P.ring_stride = (int)(std::max(merge, ring) + 127) / 128 * 128;
-  P.res_at = P.ring_at + W * P.ring_stride;
-  const size_t smem = P.res_at + (P.splits > 1 ? (size_t)C * D * 4 : 0);
+  const size_t smem = P.ring_at + (size_t)L.W * P.ring_stride;
   const void* fn = (const void*)kv4_attention_kernel<NG, NT, QT, PT>;
   cudaError_t e = ops4_smem_limit(fn, smem);
   if (e != cudaSuccess) return e;
+  void* args[] = {&P};
+  e = cudaLaunchKernel(fn, dim3((unsigned)(L.units * P.splits)), dim3(32 * L.W), args, smem, s);
+  if (e != cudaSuccess || P.splits == 1) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * P.splits));
-  cfg.blockDim = dim3(32 * W);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3((unsigned)(L.units * C / 4));
+  cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = P.splits;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = P.splits > 1 ? 1 : 0;
-  void* args[] = {&P};
-  return cudaLaunchKernelExC(&cfg, fn, args);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, (const void*)kv4_join_kernel<NG, NT>, args);
 }
 
 template <int NG, int QT, int PT>
-static cudaError_t launch_attention_nt(int NT, Kv4Attn& P, int W, long long units, cudaStream_t s) {
-  if (NT == 1) return launch_attention<NG, 1, QT, PT>(P, W, units, s);
-  if (NT == 2 || NG == 8) return launch_attention<NG, 2, QT, PT>(P, W, units, s);
-  return launch_attention<NG, NG == 8 ? 2 : 4, QT, PT>(P, W, units, s);
+static cudaError_t launch_attention_nt(Kv4Attn& P, const Kv4Plan& L, int sms, cudaStream_t s) {
+  if (L.NT == 1) return launch_attention<NG, 1, QT, PT>(P, L, sms, s);
+  if constexpr (NG == 4 && QT == 1)
+    if (L.NT == 4) return launch_attention<NG, 4, QT, PT>(P, L, sms, s);
+  return launch_attention<NG, 2, QT, PT>(P, L, sms, s);
 }
 
 template <int NG>
-static cudaError_t launch_attention_types(int NT, Kv4Attn& P, int W, long long units, cudaStream_t s) {
-  if (P.dtype == kF32) return launch_attention_nt<NG, 2, 2>(NT, P, W, units, s);
-  if (P.dtype == kF16) return launch_attention_nt<NG, 1, 2>(NT, P, W, units, s);
-  return launch_attention_nt<NG, 1, 1>(NT, P, W, units, s);
+static cudaError_t launch_attention_types(Kv4Attn& P, const Kv4Plan& L, int sms, cudaStream_t s) {
+  if (P.dtype == kF32) return launch_attention_nt<NG, 2, 2>(P, L, sms, s);
+  if (P.dtype == kF16) return launch_attention_nt<NG, 1, 2>(P, L, sms, s);
+  return launch_attention_nt<NG, 1, 1>(P, L, sms, s);
 }
 
 cudaError_t launch_kv4_attention(const Kv4Shape& S, const Kv4Attention& A, int sms, cudaStream_t s) {
@@ -775,25 +962,19 @@ cudaError_t launch_kv4_attention(const Kv4Shape& S, const Kv4Attention& A, int s
   P.q = A.q; P.o = A.o; P.lse = A.lse;
   P.kv_len = A.kv_len; P.n_rows = A.n_rows; P.mask = A.mask;
   P.qs = A.qs; P.os = A.os;
-  P.scale_log2e = A.scale * 1.4426950408889634f;
+  P.scale_log2e = fabsf(A.scale) * 1.4426950408889634f;
+  P.negative = A.scale < 0.0f;
   P.M = A.M; P.nq = A.nq; P.grp = A.nq / S.nkv; P.dtype = A.dtype;
   P.qvec = A.qs % 4 == 0;
-  // query rows per CTA: the MMA's 8 columns, or 16, or 32 (16 where the accumulators of 256 channels fill the registers)
-  const int rows = A.M * P.grp;
-  const int NT = rows <= 8 ? 1 : (rows <= 16 || S.d == 256 ? 2 : 4);
-  P.row_tiles = (rows + 8 * NT - 1) / (8 * NT);
-  const long long units = (long long)A.B * S.nkv * P.row_tiles;
-  // Warps: two tiles each at least.  CTAs per sequence: enough to fill the
-  // SMs, while every warp keeps four tiles.
-  const int tiles = A.max_pages * (S.page_size / 16);
-  int W = 1;
-  while (W < 8 && 4 * W <= tiles) W *= 2;
-  P.splits = 1;
-  while (P.splits < 8 && units * P.splits * 2 <= 2ll * sms && tiles / (P.splits * 2) >= 4 * W) P.splits *= 2;
+  P.ovec = A.os % 4 == 0;
+  const Kv4Plan L = kv4_plan(S, A.max_pages, A.B, A.M, A.nq, A.dtype, sms);
+  P.row_tiles = L.row_tiles;
+  P.splits = L.splits;
+  P.part = static_cast<float*>(A.work);
   switch (S.d) {
-    case 64: return launch_attention_types<2>(NT, P, W, units, s);
-    case 128: return launch_attention_types<4>(NT, P, W, units, s);
-    default: return launch_attention_types<8>(NT, P, W, units, s);
+    case 64: return launch_attention_types<2>(P, L, sms, s);
+    case 128: return launch_attention_types<4>(P, L, sms, s);
+    default: return launch_attention_types<8>(P, L, sms, s);
   }
 }
 

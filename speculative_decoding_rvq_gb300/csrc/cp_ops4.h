@@ -39,7 +39,9 @@ struct Kv4Attention {
   long long qs, os;
   int max_pages, B, M, nq, dtype;
   float scale;
+  void* work;  // kv4_attention_work bytes
 };
+size_t kv4_attention_work(const Kv4Shape& S, int max_pages, int B, int M, int nq, int dtype, int sms);
 cudaError_t launch_kv4_attention(const Kv4Shape& S, const Kv4Attention& A, int sms, cudaStream_t s);
 
 }  // namespace cpk_host

@@ -752,21 +752,28 @@ cp_spec_status check_kv4(const cp_spec_kv4* S) {
   return CP_SPEC_OK;
 }
 
-// The parts that every call on a cache shares.
-cp_spec_status check_kv4_call(const cp_spec_kv4* S, const void* cache, const int32_t* pages, int32_t max_pages, int32_t n_seqs,
-                              int32_t rows, int32_t dtype) {
+// The parts that every call on a cache shares: sizes, then pointers.
+cp_spec_status check_kv4_sizes(const cp_spec_kv4* S, int32_t max_pages, int32_t n_seqs, int32_t rows, int32_t dtype) {
   cp_spec_status v = check_kv4(S);
   if (v != CP_SPEC_OK) return v;
   if (!dtype_ok(dtype)) return fail(nullptr, CP_SPEC_E_INVALID, "dtype must be 0 (fp32), 1 (bf16) or 2 (fp16)");
   if (n_seqs < 0 || rows < 0) return fail(nullptr, CP_SPEC_E_INVALID, "n_seqs and the number of rows must be >= 0");
   if (max_pages < 1 || (long long)max_pages * S->page_size > 0x7FFFFFFFll)
     return fail(nullptr, CP_SPEC_E_INVALID, "max_pages must be >= 1 with max_pages * page_size below 2^31");
+  if (((long long)rows / 2 + 1) * S->n_kv_heads * S->head_dim > (1ll << 32))
+    return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "too many rows for one launch");
+  return CP_SPEC_OK;
+}
+cp_spec_status check_kv4_cache(const cp_spec_kv4* S, const void* cache, const int32_t* pages, int32_t max_pages, int32_t n_seqs) {
   if (bad_ptr(cache) || (pages && !aligned16(pages))) return fail(nullptr, CP_SPEC_E_INVALID, "cache or page table null or misaligned");
   if (!pages && (long long)n_seqs * max_pages > S->n_pages)
     return fail(nullptr, CP_SPEC_E_INVALID, "without a page table n_seqs * max_pages must not exceed n_pages");
-  if ((long long)n_seqs * ((long long)rows / 2 + 1) > (1ll << 38) / ((long long)S->n_kv_heads * S->head_dim))
-    return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "too many rows for one launch");
   return CP_SPEC_OK;
+}
+cp_spec_status check_kv4_call(const cp_spec_kv4* S, const void* cache, const int32_t* pages, int32_t max_pages, int32_t n_seqs,
+                              int32_t rows, int32_t dtype) {
+  cp_spec_status v = check_kv4_sizes(S, max_pages, n_seqs, rows, dtype);
+  return v == CP_SPEC_OK ? check_kv4_cache(S, cache, pages, max_pages, n_seqs) : v;
 }
 
 cpk_host::Kv4Shape kv4_shape(const cp_spec_kv4* S) {
@@ -852,23 +859,40 @@ cp_spec_status cp_spec_kv4_read(const cp_spec_kv4* shape, const void* d_cache, c
                   "kv4 read launch");
 }
 
+// What kv4 attention and its workspace query share.
+static cp_spec_status check_kv4_heads(const cp_spec_kv4* S, int32_t max_pages, int32_t n_seqs, int32_t rows, int32_t n_q_heads,
+                                      int32_t dtype) {
+  cp_spec_status v = check_kv4_sizes(S, max_pages, n_seqs, rows, dtype);
+  if (v != CP_SPEC_OK) return v;
+  if (rows > CP_SPEC_MAX_KV4_ROWS) return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "rows must be <= %d", CP_SPEC_MAX_KV4_ROWS);
+  if (n_q_heads < 1 || n_q_heads % S->n_kv_heads || n_q_heads > 4096)
+    return fail(nullptr, CP_SPEC_E_INVALID, "n_q_heads must be a positive multiple of n_kv_heads, at most 4096");
+  if ((long long)n_seqs * rows * n_q_heads > (1ll << 27)) return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "too many query rows");
+  return CP_SPEC_OK;
+}
+
+size_t cp_spec_kv4_attention_bytes(const cp_spec_kv4* shape, int32_t max_pages, int32_t n_seqs, int32_t rows, int32_t n_q_heads,
+                                   int32_t dtype) {
+  if (check_kv4_heads(shape, max_pages, n_seqs, rows, n_q_heads, dtype) != CP_SPEC_OK || n_seqs == 0 || rows == 0) return 0;
+  int sms = 0;
+  if (device_sms(&sms) != cudaSuccess) return 0;
+  return cpk_host::kv4_attention_work(kv4_shape(shape), max_pages, n_seqs, rows, n_q_heads, dtype, sms);
+}
+
 cp_spec_status cp_spec_kv4_attention(const cp_spec_kv4* shape, const void* d_cache, const int32_t* d_pages, int32_t max_pages,
                                      int32_t n_seqs, int32_t rows, int32_t n_q_heads, const int32_t* d_kv_len,
                                      const int32_t* d_rows, const uint64_t* d_mask, float scale, int32_t dtype,
                                      const void* d_q, int64_t q_stride, void* d_o, int64_t o_stride, float* d_lse,
-                                     void* stream) {
-  cp_spec_status v = check_kv4_call(shape, d_cache, d_pages, max_pages, n_seqs, rows, dtype);
+                                     void* d_work, size_t work_bytes, void* stream) {
+  cp_spec_status v = check_kv4_heads(shape, max_pages, n_seqs, rows, n_q_heads, dtype);
+  if (v == CP_SPEC_OK) v = check_kv4_cache(shape, d_cache, d_pages, max_pages, n_seqs);
   if (v != CP_SPEC_OK) return v;
-  if (rows > CP_SPEC_MAX_KV4_ROWS) return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "rows must be <= %d", CP_SPEC_MAX_KV4_ROWS);
-  if (n_q_heads < 1 || n_q_heads % shape->n_kv_heads || n_q_heads > 4096)
-    return fail(nullptr, CP_SPEC_E_INVALID, "n_q_heads must be a positive multiple of n_kv_heads, at most 4096");
   if (!std::isfinite(scale)) return fail(nullptr, CP_SPEC_E_INVALID, "scale must be finite");
   const int64_t width = (int64_t)n_q_heads * shape->head_dim;
   if (q_stride < width || o_stride < width) return fail(nullptr, CP_SPEC_E_INVALID, "row strides must cover a row");
   if (n_seqs == 0 || rows == 0) return CP_SPEC_OK;
-  if ((long long)n_seqs * rows * n_q_heads > (1ll << 27)) return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "too many query rows");
   if (bad_ptr(d_kv_len) || (d_rows && !aligned16(d_rows)) || (d_mask && !aligned16(d_mask)) || bad_ptr(d_q) || bad_ptr(d_o) ||
-      (d_lse && !aligned16(d_lse)))
+      (d_lse && !aligned16(d_lse)) || (d_work && !aligned16(d_work)))
     return fail(nullptr, CP_SPEC_E_INVALID, "null or misaligned pointer");
   int sms = 0;
   cudaError_t e = device_sms(&sms);
@@ -880,6 +904,10 @@ cp_spec_status cp_spec_kv4_attention(const cp_spec_kv4* shape, const void* d_cac
   A.qs = q_stride; A.os = o_stride;
   A.max_pages = max_pages; A.B = n_seqs; A.M = rows; A.nq = n_q_heads; A.dtype = dtype;
   A.scale = scale;
+  A.work = d_work;
+  const size_t need = cpk_host::kv4_attention_work(kv4_shape(shape), max_pages, n_seqs, rows, n_q_heads, dtype, sms);
+  if (need > (d_work ? work_bytes : 0))
+    return fail(nullptr, CP_SPEC_E_WORKSPACE, "needs %zu bytes of workspace (cp_spec_kv4_attention_bytes)", need);
   return launched(cpk_host::launch_kv4_attention(kv4_shape(shape), A, sms, static_cast<cudaStream_t>(stream)),
                   "kv4 attention launch");
 }

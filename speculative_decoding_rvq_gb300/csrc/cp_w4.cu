@@ -8,6 +8,7 @@
 // holds 16 bytes of row g and 16 bytes of row g + 8, one 32-bit word per 32
 // columns, the word's byte j holding columns 8 t + 2 j and 8 t + 2 j + 1.
 // Rows and columns past the matrix are zero codes with zero scales.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -23,8 +24,12 @@ namespace cpk {
 constexpr int kW4Warps = 8;
 constexpr int kW4Threads = 32 * kW4Warps;
 constexpr int kW4TileK = 128;
-constexpr int kW4Stages = 6;  // tiles in flight per warp
 
+// Tiles of 16 rows that a warp multiplies at once, by the MMA column tiles NT
+// of x: two where there are many columns, so that a fragment of x read from
+// shared memory serves two MMAs; and the tiles in flight per warp.
+__host__ __device__ constexpr int w4_mt(int NT) { return NT == 4 ? 2 : 1; }
+__host__ __device__ constexpr int w4_stages(int NT) { return NT == 4 ? 3 : 6; }
 __host__ __device__ inline int w4_groups(int group) { return kW4TileK / group; }  // scales per tile row
 __host__ __device__ inline int w4_tile_bytes(int group) { return 1024 + 32 * w4_groups(group); }
 // Byte offset of the scale of row i (0..15), group q of a tile.
@@ -90,11 +95,12 @@ __global__ void __launch_bounds__(256) w4_unpack_kernel(const unsigned char* pac
 
 // ---------------------------------------------------------------- product
 // Tensor-core product of few rows.  A CTA of 8 warps takes `rb` rows of x and
-// walks over groups of 16-row tiles of w: WK of its warps split K, the other
-// factor takes neighbouring tiles.  A warp streams its tiles through a ring
-// of kW4Stages asynchronous copies in shared memory, turns codes into fp16
-// (exact), and multiplies them with the rows of x, which are the N operand
-// (8 columns per MMA).
+// walks over groups of 16-row tiles of w: WK of its warps split its share of
+// K, the other factor takes neighbouring tiles; the CTAs of a cluster split K
+// further.  A warp streams its tiles through a ring of kW4Stages asynchronous
+// copies in shared memory, turns codes into fp16 (exact), and multiplies them
+// with the rows of x, which are the N operand (8 columns per MMA).  Shares of
+// K are added in a fixed order through (distributed) shared memory.
 //
 // The rows of x are held as fp16, each block of 128 columns scaled by a power
 // of two that the result is scaled back by: bfloat16 and fp16 inputs exactly
@@ -111,77 +117,175 @@ struct W4Gemv {
   const unsigned char* w;
   void* y;
   long long xs, ys;  // row strides, in elements
-  int R, N, K, KB, group;
+  int R, N, K, KB;
   int xdt, ydt;
   int rb;       // rows of x per CTA
   int XS;       // bytes of one column of x in shared memory
-  int wk;       // warps that split K
+  int wk, ck;   // warps of a CTA and CTAs of a cluster that split K
   int ring_at, red_at, fac_at;  // shared-memory offsets
   bool xvec;
 };
 
-template <int NT, int TERMS>
-__global__ void __launch_bounds__(kW4Threads, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) w4_gemv_kernel(const __grid_constant__ W4Gemv P) {
-  extern __shared__ __align__(128) unsigned char sm[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int WK = P.wk, WM = kW4Warps / WK, wk = warp % WK, wm = warp / WK;
-  const int r0 = blockIdx.y * P.rb, rows = min(P.rb, P.R - r0), cols = rows * TERMS;
-  const int tiles = (P.N + 15) / 16, groups = (tiles + WM - 1) / WM;  // tile groups of WM neighbouring tiles
-  const int kb0 = (int)((long long)P.KB * wk / WK), nb = (int)((long long)P.KB * (wk + 1) / WK) - kb0;
-  const int ns = w4_groups(P.group), tb = w4_tile_bytes(P.group);
-  const int mine = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // groups of this CTA
-  unsigned char* ring = sm + P.ring_at + (size_t)warp * kW4Stages * tb;
-  float* fac = reinterpret_cast<float*>(sm + P.fac_at);  // [KB][rb] powers of two
-  float* red = reinterpret_cast<float*>(sm + P.red_at);  // [2][8 warps][16][rb]
-
-  // items: this warp's tile of each group, block by block; an item past the matrix copies nothing
-  const int items = mine * nb;
-  int ij = 0, ib = 0;  // group and block of the next copy
-  auto issue = [&](int q) {
-    if (q < items) {
-      const int tile = ((int)blockIdx.x + ij * (int)gridDim.x) * WM + wm;
-      if (tile < tiles) {
-        const unsigned char* src = P.w + ((long long)tile * P.KB + kb0 + ib) * tb;
-        unsigned char* dst = ring + (q % kW4Stages) * tb;
-        cp_async16(dst + lane * 16, src + lane * 16);
-        cp_async16(dst + 512 + lane * 16, src + 512 + lane * 16);
-        if (lane < 2 * ns) cp_async16(dst + 1024 + lane * 16, src + 1024 + lane * 16);
-      }
-      if (++ib == nb) { ib = 0; ++ij; }
+// Eight consecutive elements of a row as they are stored (16-bit types in the
+// first four words), zeros at and past n.
+template <int TERMS>
+__device__ __forceinline__ void load8(const void* row, int k0, int n, bool vec, uint32_t (&v)[TERMS == 2 ? 8 : 4]) {
+  if constexpr (TERMS == 2) {
+    const uint32_t* p = static_cast<const uint32_t*>(row) + k0;
+    if (vec && k0 + 7 < n) {
+      const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 4);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      return;
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = k0 + i < n ? p[i] : 0u;
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(row) + k0;
+    if (vec && k0 + 7 < n) {
+      const uint4 a = *reinterpret_cast<const uint4*>(p);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = (k0 + 2 * i < n ? p[2 * i] : 0u) | (k0 + 2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+  }
+}
+
+// One warp's pair of blocks of a row of x, eight elements a lane, to fp16
+// scaled by a power of two per block (half a warp): returns its inverse.
+// Where a block holds an infinity or a NaN the finite elements set the power.
+template <int TERMS>
+__device__ __forceinline__ float convert8(const uint32_t (&v)[TERMS == 2 ? 8 : 4], bool bf16, uint4* hi, uint4* lo) {
+  float f[8];
+  uint32_t top = 0, limit = 0x7F800000u;  // the largest magnitude's bits, and where the numbers that are not finite begin
+  if constexpr (TERMS == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      f[i] = __uint_as_float(v[i]);
+      top = max(top, v[i] & 0x7FFFFFFFu);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      top = __vmaxu2(top, v[i] & 0x7FFF7FFFu);
+      const float2 x = bf16 ? bf16x2_to_f2(v[i]) : unpack_half2(v[i]);
+      f[2 * i] = x.x;
+      f[2 * i + 1] = x.y;
+    }
+    top = max(top & 0xFFFFu, top >> 16);
+    limit = bf16 ? 0x7F80u : 0x7C00u;
+  }
+  const bool odd = __any_sync(0xffffffffu, top >= limit);
+  if (odd) {
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, finite_abs_bits(f[i]));
+  } else if (TERMS == 1) {
+    top = bf16 ? top << 16 : __float_as_uint(__half2float(__ushort_as_half((unsigned short)top)));
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float up, down;
+  pow2_normaliser(top, &up, &down);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] *= up;
+  *hi = make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
+  if constexpr (TERMS == 2) {
+    const uint32_t h[4] = {hi->x, hi->y, hi->z, hi->w};
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack_half2(h[i]);
+      float a = f[2 * i] - x.x, c = f[2 * i + 1] - x.y;
+      if (odd) {
+        a = fp16_rest(f[2 * i]);
+        c = fp16_rest(f[2 * i + 1]);
+      }
+      r[i] = pack_half2(a, c);
+    }
+    *lo = make_uint4(r[0], r[1], r[2], r[3]);
+  }
+  return down;
+}
+
+template <int NT, int TERMS, int NS>
+__global__ void __launch_bounds__(kW4Threads, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) w4_gemv_kernel(const __grid_constant__ W4Gemv P) {
+  constexpr int TB = 1024 + 32 * NS, MT = w4_mt(NT), ST = w4_stages(NT);
+  extern __shared__ __align__(128) unsigned char sm[];
+  namespace cg = cooperative_groups;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int WK = P.wk, CK = P.ck, WM = kW4Warps / WK, wk = warp % WK, wm = warp / WK;
+  const int cr = CK > 1 ? (int)blockIdx.x % CK : 0, cx = (int)blockIdx.x / CK, gx = (int)gridDim.x / CK;
+  const int r0 = blockIdx.y * P.rb, rows = min(P.rb, P.R - r0), cols = rows * TERMS;
+  const int tiles = (P.N + 15) / 16, groups = (tiles + WM * MT - 1) / (WM * MT);  // groups of WM * MT neighbouring tiles
+  const int shares = CK * WK, share = cr * WK + wk;
+  const int kb0 = (int)((long long)P.KB * share / shares), nb = (int)((long long)P.KB * (share + 1) / shares) - kb0;
+  const int cb0 = (int)((long long)P.KB * cr / CK), cnb = (int)((long long)P.KB * (cr + 1) / CK) - cb0;  // the CTA's blocks
+  const int mine = (groups - cx + gx - 1) / gx;  // groups of this CTA
+  unsigned char* ring = sm + P.ring_at + (size_t)warp * ST * MT * TB;
+  float* fac = reinterpret_cast<float*>(sm + P.fac_at);  // [blocks of the CTA][rb] powers of two
+  float* red = reinterpret_cast<float*>(sm + P.red_at);  // [2][8 warps][MT][rb][16]
+
+  // copies: this warp's tiles of each group, block by block; a tile past the matrix copies nothing
+  int left = nb;  // blocks left in the tiles being copied
+  int ctile = (cx * WM + wm) * MT, cslot = 0;
+  const long long tile_stride = (long long)P.KB * TB;
+  const unsigned char* src = P.w + ctile * tile_stride + (long long)kb0 * TB + lane * 16;
+  const long long jump = gx * WM * MT * tile_stride - (long long)nb * TB;
+  auto issue = [&]() {
+    if (ctile < tiles) {
+      unsigned char* dst = ring + cslot * (MT * TB) + lane * 16;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        if (m == 0 || ctile + m < tiles) {
+          const unsigned char* from = src + m * tile_stride;
+          cp_async16(dst + m * TB, from);
+          cp_async16(dst + m * TB + 512, from + 512);
+          if (lane < 2 * NS) cp_async16(dst + m * TB + 1024, from + 1024);
+        }
+      src += TB;
+      if (--left == 0) {
+        left = nb;
+        src += jump;
+        ctile += gx * WM * MT;
+      }
+    }
+    cslot = cslot + 1 == ST ? 0 : cslot + 1;
     cp_async_commit();
   };
-  for (int q = 0; q < kW4Stages - 1; ++q) issue(q);
+#pragma unroll 1
+  for (int q = 0; q < ST - 1; ++q) issue();
 
-  // x: one warp per (row, block of 128 columns), four elements a lane
+  // x: one warp per (row, two blocks of 128 columns), eight elements a lane
   {
-    const int units = rows * P.KB, es = elem_bytes(P.xdt);
-    for (int u0 = warp; u0 < units; u0 += 4 * kW4Warps) {
-      float4 v[4];
+    constexpr int U = NT == 4 ? 8 : 4;
+    const unsigned pairs = (cnb + 1) / 2, inverse = 0xFFFFFFFFu / pairs + 1u;  // u / pairs by a product (u * pairs < 2^32)
+    const int units = rows * (int)pairs;
+    const long long row_bytes = P.xs * (TERMS == 2 ? 4 : 2);
+    const unsigned char* x0 = static_cast<const unsigned char*>(P.x) + r0 * row_bytes;
+    const int kl0 = lane >> 4, at = (lane & 15) * 8;
+    for (int u0 = warp; u0 < units; u0 += U * kW4Warps) {
+      uint32_t v[U][TERMS == 2 ? 8 : 4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int u = u0 + i * kW4Warps;
-        if (u >= units) continue;
-        const int r = u / P.KB, kb = u - r * P.KB;
-        v[i] = load4(static_cast<const unsigned char*>(P.x) + (long long)(r0 + r) * P.xs * es, P.xdt,
-                     kb * kW4TileK + lane * 4, P.K, P.xvec);
+      for (int i = 0; i < U; ++i) {
+        const unsigned u = u0 + i * kW4Warps, r = pairs == 1 ? u : __umulhi(u, inverse);
+        if ((int)u < units) load8<TERMS>(x0 + r * row_bytes, (cb0 + 2 * (int)(u - r * pairs) + kl0) * kW4TileK + at, P.K, P.xvec, v[i]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int u = u0 + i * kW4Warps;
-        if (u >= units) continue;
-        const int r = u / P.KB, kb = u - r * P.KB;
-        const uint32_t m = max(max(finite_abs_bits(v[i].x), finite_abs_bits(v[i].y)),
-                               max(finite_abs_bits(v[i].z), finite_abs_bits(v[i].w)));
-        float up, down;
-        pow2_normaliser(__reduce_max_sync(0xffffffffu, m), &up, &down);
-        if (lane == 0) fac[kb * P.rb + r] = down;
-        const float a = v[i].x * up, b = v[i].y * up, c = v[i].z * up, d = v[i].w * up;
-        unsigned char* dst = sm + (size_t)(r * TERMS) * P.XS + kb * 256 + lane * 8;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_half2(a, b), pack_half2(c, d));
-        if (TERMS == 2)
-          *reinterpret_cast<uint2*>(dst + P.XS) =
-              make_uint2(pack_half2(fp16_rest(a), fp16_rest(b)), pack_half2(fp16_rest(c), fp16_rest(d)));
+      for (int i = 0; i < U; ++i) {
+        const unsigned u = u0 + i * kW4Warps, r = pairs == 1 ? u : __umulhi(u, inverse);
+        if ((int)u >= units) break;
+        const int kl = 2 * (int)(u - r * pairs) + kl0;
+        uint4 hi, lo;
+        const float down = convert8<TERMS>(v[i], P.xdt == kBF16, &hi, &lo);
+        if (kl < cnb) {
+          unsigned char* dst = sm + (int)r * TERMS * P.XS + kl * 256 + at * 2;
+          *reinterpret_cast<uint4*>(dst) = hi;
+          if (TERMS == 2) *reinterpret_cast<uint4*>(dst + P.XS) = lo;
+          if (at == 0) fac[kl * P.rb + r] = down;
+        }
       }
     }
   }
@@ -191,122 +295,159 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) w
   // accumulator columns (a column past the rows repeats the last one and is
   // never stored)
   const unsigned char* xcol[NT];
-  int arow[NT][2];
+  const float* fcol[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    xcol[n] = sm + (size_t)min(n * 8 + g, cols - 1) * P.XS + t * 16;
+    xcol[n] = sm + (size_t)min(n * 8 + g, cols - 1) * P.XS + (kb0 - cb0) * 256 + t * 16;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) arow[n][c] = min(n * 8 + 2 * t + c, cols - 1) / TERMS;
+    for (int c = 0; c < 2; ++c) fcol[n][c] = fac + (kb0 - cb0) * P.rb + min(n * 8 + 2 * t + c, cols - 1) / TERMS;
   }
 
-  int q = 0;
+  int slot = 0;
+#pragma unroll 1
   for (int j = 0; j < mine; ++j) {
-    const int tile = ((int)blockIdx.x + j * (int)gridDim.x) * WM + wm;
-    float tot[NT][4];
+    const int tile = ((cx + j * gx) * WM + wm) * MT;
+    float tot[MT][NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tot[n][c] = 0.0f;
-    for (int b = 0; b < nb; ++b, ++q) {
-      cp_async_wait_group<kW4Stages - 2>();
-      __syncwarp();
-      const unsigned char* st = ring + (q % kW4Stages) * tb;
-      const uint4 lo4 = *reinterpret_cast<const uint4*>(st + lane * 16);
-      const uint4 hi4 = *reinterpret_cast<const uint4*>(st + 512 + lane * 16);
-      uint32_t slo[2], shi[2];  // scales of rows g and g + 8, two to a word
-      if (ns == 4) {
-        const uint2 a = *reinterpret_cast<const uint2*>(st + w4_scale_at(g, 0, 4));
-        const uint2 c = *reinterpret_cast<const uint2*>(st + w4_scale_at(g + 8, 0, 4));
-        slo[0] = a.x; slo[1] = a.y; shi[0] = c.x; shi[1] = c.y;
-      } else if (ns == 2) {
-        slo[0] = *reinterpret_cast<const uint32_t*>(st + w4_scale_at(g, 0, 2));
-        shi[0] = *reinterpret_cast<const uint32_t*>(st + w4_scale_at(g + 8, 0, 2));
-        slo[1] = shi[1] = 0;
-      } else {
-        slo[0] = *reinterpret_cast<const uint16_t*>(st + w4_scale_at(g, 0, 1));
-        shi[0] = *reinterpret_cast<const uint16_t*>(st + w4_scale_at(g + 8, 0, 1));
-        slo[1] = shi[1] = 0;
-      }
-      __syncwarp();  // every lane has read the stage that the next copy may reuse
-      issue(q + kW4Stages - 1);
-      if (tile >= tiles) continue;
-      const int kb = kb0 + b;
-      const uint32_t lw[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hw[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
-      float blk[NT][4], acc[NT][4];
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) blk[n][c] = acc[n][c] = 0.0f;
+        for (int c = 0; c < 4; ++c) tot[m][n][c] = 0.0f;
+    if (tile < tiles)
+#pragma unroll 1
+      for (int b = 0; b < nb; ++b) {
+        cp_async_wait_group<ST - 2>();
+        __syncwarp();
+        const unsigned char* st = ring + slot * (MT * TB);
+        slot = slot + 1 == ST ? 0 : slot + 1;
+        uint32_t lw[MT][4], hw[MT][4];                          // codes of rows g and g + 8
+        uint32_t slo[MT][(NS + 1) / 2], shi[MT][(NS + 1) / 2];  // their scales, two to a word
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t al[4], ah[4];
-        e2m1_to_half2x4(lw[w], al);
-        e2m1_to_half2x4(hw[w], ah);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint4 x4 = *reinterpret_cast<const uint4*>(xcol[n] + kb * 256 + w * 64);
-          mma_f16_16816(acc[n], al[0], ah[0], al[1], ah[1], x4.x, x4.y);
-          mma_f16_16816(acc[n], al[2], ah[2], al[3], ah[3], x4.z, x4.w);
-        }
-        if (((w + 1) & (4 / ns - 1)) == 0) {  // the end of a group
-          const int s = (w + 1) * ns / 4 - 1;
-          const float a = bf16_bits_f32((slo[s >> 1] >> (16 * (s & 1))) & 0xFFFFu);
-          const float c = bf16_bits_f32((shi[s >> 1] >> (16 * (s & 1))) & 0xFFFFu);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            blk[n][0] = fmaf(a, acc[n][0], blk[n][0]);
-            blk[n][1] = fmaf(a, acc[n][1], blk[n][1]);
-            blk[n][2] = fmaf(c, acc[n][2], blk[n][2]);
-            blk[n][3] = fmaf(c, acc[n][3], blk[n][3]);
-            acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+        for (int m = 0; m < MT; ++m) {
+          const unsigned char* T = st + m * TB;
+          const uint4 lo4 = *reinterpret_cast<const uint4*>(T + lane * 16);
+          const uint4 hi4 = *reinterpret_cast<const uint4*>(T + 512 + lane * 16);
+          lw[m][0] = lo4.x; lw[m][1] = lo4.y; lw[m][2] = lo4.z; lw[m][3] = lo4.w;
+          hw[m][0] = hi4.x; hw[m][1] = hi4.y; hw[m][2] = hi4.z; hw[m][3] = hi4.w;
+          if constexpr (NS == 4) {
+            const uint2 a = *reinterpret_cast<const uint2*>(T + w4_scale_at(g, 0, 4));
+            const uint2 c = *reinterpret_cast<const uint2*>(T + w4_scale_at(g + 8, 0, 4));
+            slo[m][0] = a.x; slo[m][1] = a.y; shi[m][0] = c.x; shi[m][1] = c.y;
+          } else if constexpr (NS == 2) {
+            slo[m][0] = *reinterpret_cast<const uint32_t*>(T + w4_scale_at(g, 0, 2));
+            shi[m][0] = *reinterpret_cast<const uint32_t*>(T + w4_scale_at(g + 8, 0, 2));
+          } else {
+            slo[m][0] = *reinterpret_cast<const uint16_t*>(T + w4_scale_at(g, 0, 1));
+            shi[m][0] = *reinterpret_cast<const uint16_t*>(T + w4_scale_at(g + 8, 0, 1));
           }
         }
-      }
+        __syncwarp();  // every lane has read the stage that the next copy may reuse
+        issue();
+        float blk[MT][NT][4], acc[MT][NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float f0 = fac[kb * P.rb + arow[n][0]], f1 = fac[kb * P.rb + arow[n][1]];
-        tot[n][0] = fmaf(f0, blk[n][0], tot[n][0]);
-        tot[n][1] = fmaf(f1, blk[n][1], tot[n][1]);
-        tot[n][2] = fmaf(f0, blk[n][2], tot[n][2]);
-        tot[n][3] = fmaf(f1, blk[n][3], tot[n][3]);
-      }
-    }
-    // the tile's outputs: hi and lo columns of a row sit in one thread
-    float* mine_red = red + ((j & 1) * kW4Warps + warp) * 16 * P.rb;
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = g + 8 * h;
+            for (int c = 0; c < 4; ++c) blk[m][n][c] = acc[m][n][c] = 0.0f;
 #pragma unroll
-        for (int c = 0; c < 2 / TERMS; ++c) {
-          const int r = (n * 8 + 2 * t) / TERMS + c;
-          const float v = TERMS == 2 ? tot[n][2 * h] + tot[n][2 * h + 1] : tot[n][2 * h + c];
-          if (r < rows) {
-            if (WK == 1) {
-              const int o = tile * 16 + row;
-              if (o < P.N) store_elem(P.y, (long long)(r0 + r) * P.ys + o, P.ydt, v);
-            } else {
-              mine_red[r * 16 + row] = v;
+        for (int w = 0; w < 4; ++w) {
+          uint32_t al[MT][4], ah[MT][4];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            e2m1_to_half2x4(lw[m][w], al[m]);
+            e2m1_to_half2x4(hw[m][w], ah[m]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint4 x4 = *reinterpret_cast<const uint4*>(xcol[n] + b * 256 + w * 64);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              mma_f16_16816(acc[m][n], al[m][0], ah[m][0], al[m][1], ah[m][1], x4.x, x4.y);
+              mma_f16_16816(acc[m][n], al[m][2], ah[m][2], al[m][3], ah[m][3], x4.z, x4.w);
+            }
+          }
+          if (((w + 1) & (4 / NS - 1)) == 0) {  // the end of a group
+            constexpr int per = 4 / NS;
+            const int q = (w + 1) / per - 1;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              const float a = __uint_as_float((q & 1) ? slo[m][q >> 1] & 0xFFFF0000u : slo[m][q >> 1] << 16);
+              const float c = __uint_as_float((q & 1) ? shi[m][q >> 1] & 0xFFFF0000u : shi[m][q >> 1] << 16);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                blk[m][n][0] = fmaf(a, acc[m][n][0], blk[m][n][0]);
+                blk[m][n][1] = fmaf(a, acc[m][n][1], blk[m][n][1]);
+                blk[m][n][2] = fmaf(c, acc[m][n][2], blk[m][n][2]);
+                blk[m][n][3] = fmaf(c, acc[m][n][3], blk[m][n][3]);
+                acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.0f;
+              }
             }
           }
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float f0 = fcol[n][0][b * P.rb], f1 = fcol[n][1][b * P.rb];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            tot[m][n][0] = fmaf(f0, blk[m][n][0], tot[m][n][0]);
+            tot[m][n][1] = fmaf(f1, blk[m][n][1], tot[m][n][1]);
+            tot[m][n][2] = fmaf(f0, blk[m][n][2], tot[m][n][2]);
+            tot[m][n][3] = fmaf(f1, blk[m][n][3], tot[m][n][3]);
+          }
+        }
       }
-    }
-    if (WK > 1) {  // add the K shares in warp order; the buffer of this parity is free again two groups on
-      __syncthreads();
-      const int outs = rows * 16 * WM;
-      for (int i = tid; i < outs; i += kW4Threads) {
-        const int m = i / (rows * 16), rest = i - m * rows * 16;  // rest = r * 16 + row
-        const float* src = red + ((j & 1) * kW4Warps + m * WK) * 16 * P.rb + rest;
+    // the tiles' outputs: hi and lo columns of a row sit in one thread
+    float* part = red + ((j & 1) * kW4Warps + warp) * (MT * 16) * P.rb;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 0; c < 2 / TERMS; ++c) {
+            const int row = g + 8 * h, r = (n * 8 + 2 * t) / TERMS + c;
+            const float v = TERMS == 2 ? tot[m][n][2 * h] + tot[m][n][2 * h + 1] : tot[m][n][2 * h + c];
+            if (r < rows) {
+              if (shares == 1) {
+                const int o = (tile + m) * 16 + row;
+                if (o < P.N) store_elem(P.y, (long long)(r0 + r) * P.ys + o, P.ydt, v);
+              } else {
+                part[(m * P.rb + r) * 16 + row] = v;
+              }
+            }
+          }
+    if (shares > 1) {  // add the shares of K in order; the buffer of this parity is free again two groups on
+      const int outs = rows * 16 * WM * MT;
+      const float* from = red + (j & 1) * kW4Warps * (MT * 16) * P.rb;
+      if (CK == 1) __syncthreads();
+      else cg::this_cluster().sync();
+      for (int i = cr * kW4Threads + tid; i < outs; i += CK * kW4Threads) {
+        const int m = i / (rows * 16), rest = i - m * rows * 16;  // m: tile of the group; rest = r * 16 + row
+        const float* at = from + ((m / MT) * WK * MT + m % MT) * 16 * P.rb + rest;
         float v = 0.0f;
-        for (int k = 0; k < WK; ++k) v += src[k * 16 * P.rb];
-        const long long o = (((long long)blockIdx.x + (long long)j * gridDim.x) * WM + m) * 16 + (rest & 15);
+        if (CK == 1) {
+          for (int k = 0; k < WK; ++k) v += at[k * (MT * 16) * P.rb];
+        } else {
+          float f[8];
+          for (int k = 0; k < WK; ++k) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (q < CK) f[q] = *cg::this_cluster().map_shared_rank(at + k * (MT * 16) * P.rb, q);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (q < CK) v += f[q];
+          }
+        }
+        const long long o = (((long long)cx + (long long)j * gx) * (WM * MT) + m) * 16 + (rest & 15);
         if (o < P.N) store_elem(P.y, (long long)(r0 + (rest >> 4)) * P.ys + o, P.ydt, v);
       }
     }
   }
   cp_async_wait_group<0>();
+  if (CK > 1) cg::this_cluster().sync();  // no CTA leaves while another reads its shared memory
 }
 
 }  // namespace cpk
@@ -355,64 +496,133 @@ cudaError_t launch_w4_unpack(int N, int K, int group, int dtype, const void* pac
 
 // Shared memory of one CTA: the columns of x, the rings, the K shares of two
 // groups of outputs, the powers of two.
-static size_t w4_smem(W4Gemv& P, int terms) {
+static int w4_columns(const W4Gemv& P, int terms) {
+  const int cols = P.rb * terms;
+  return cols <= 8 ? 1 : (cols <= 16 ? 2 : 4);
+}
+static size_t w4_smem(W4Gemv& P, int terms, int tile_bytes) {
+  const int blocks = (P.KB + P.ck - 1) / P.ck, NT = w4_columns(P, terms), MT = w4_mt(NT);
+  // neighbouring columns half a bank row apart: a quarter warp's 16-byte reads meet no conflict
+  P.XS = blocks * 256 + 64;
   size_t at = (size_t)P.rb * terms * P.XS;
   P.ring_at = (int)at;
-  at += (size_t)kW4Warps * kW4Stages * w4_tile_bytes(P.group);
+  at += (size_t)kW4Warps * w4_stages(NT) * MT * tile_bytes;
   P.red_at = (int)at;
-  if (P.wk > 1) at += (size_t)2 * kW4Warps * 16 * P.rb * 4;
+  if (P.wk * P.ck > 1) at += (size_t)2 * kW4Warps * MT * 16 * P.rb * 4;
   P.fac_at = (int)at;
-  at += (size_t)P.KB * P.rb * 4;
+  at += (size_t)blocks * P.rb * 4;
   return (at + 127) / 128 * 128;
 }
 
+// Estimated time of a plan in clocks, fitted to times of 16 shapes (1 to 64
+// rows, matrices of 2 to 270 million weights) under every split of K: the
+// conversion of x, which every CTA does, in batches of loads; `per` groups of
+// tiles of `blocks` blocks each, bound by a block's latency or by what the
+// SM's warps issue; the joins of the shares of K.  `share`: CTAs on an SM.
+static long long w4_cost(const W4Gemv& P, int NT, int per, int blocks, int share) {
+  const int units = P.rb * (((P.KB + P.ck - 1) / P.ck + 1) / 2), batch = (NT == 4 ? 8 : 4) * kW4Warps;
+  const int load = NT == 4 ? 2450 : 1300, lat = NT == 1 ? 470 : (NT == 2 ? 700 : 1770), thr = NT == 1 ? 340 : (NT == 2 ? 420 : 2010);
+  const long long prep = (long long)(units + batch - 1) / batch * load * (3 + share) / 4 + units * 18 * share;
+  const long long outs = (long long)P.rb * 16 * (kW4Warps / P.wk) * w4_mt(NT);
+  const long long join = P.ck > 1 ? 1860 + outs * P.wk * 228 / 256 : (P.wk > 1 ? 760 + outs * P.wk * 240 / 256 : 0);
+  return prep + per * ((long long)blocks * std::max(lat, thr * share) + join);
+}
+
 constexpr size_t kW4SmemMax = 227 * 1024;
+
+// How a product is laid out: rows of x per CTA (up to 32 columns; halved where
+// that pays or has to be for x to fit), CTAs of a cluster and warps of a CTA
+// that split K, CTAs along the tiles.
+struct W4Plan {
+  int rb, ck, wk, grid;
+};
+
+static W4Plan w4_plan(int R, int N, int K, int group, int terms, int sms) {
+  W4Gemv P{};
+  P.KB = (K + kW4TileK - 1) / kW4TileK;
+  const int tb = w4_tile_bytes(group), rb_max = std::min(R, 32 / terms);
+  W4Plan best{};
+  long long best_cost = -1;
+  for (int rb = rb_max; rb >= 1; rb = rb == 1 ? 0 : (rb + 1) / 2) {
+    if (best_cost >= 0 && rb * 4 <= rb_max) break;
+    const int rblocks = (R + rb - 1) / rb;
+    P.rb = (R + rblocks - 1) / rblocks;
+    const int NT = w4_columns(P, terms), MT = w4_mt(NT), most = NT == 1 ? 3 : (NT == 2 ? 2 : 1);
+    for (P.ck = 1; P.ck <= 8 && P.ck <= P.KB; P.ck *= 2)
+      for (P.wk = 1; P.wk <= kW4Warps && P.wk * P.ck <= P.KB; P.wk *= 2) {
+        const size_t smem = w4_smem(P, terms, tb);
+        if (smem > kW4SmemMax) continue;
+        const int ctas = (int)std::max<size_t>(1, std::min<size_t>(most, kW4SmemMax / (smem + 1024)));
+        const int rows = kW4Warps / P.wk * MT * 16, groups = (N + rows - 1) / rows;
+        const int slots = std::max(1, sms * ctas / (rblocks * P.ck)), per = (groups + slots - 1) / slots;
+        const int grid = (groups + per - 1) / per * P.ck;
+        const int share = (int)std::min<long long>(ctas, ((long long)grid * rblocks + sms - 1) / sms);
+        const long long cost = w4_cost(P, NT, per, (P.KB + P.ck * P.wk - 1) / (P.ck * P.wk), share);
+        if (best_cost < 0 || cost < best_cost) {
+          best_cost = cost;
+          best = W4Plan{P.rb, P.ck, P.wk, grid};
+        }
+      }
+  }
+  return best;  // (one row of the longest K always fits: rb is never 0)
+}
+
+// The same few shapes come again with every pass: a thread keeps their plans.
+static W4Plan w4_plan_cached(int R, int N, int K, int group, int terms, int sms) {
+  struct Entry {
+    int R, N, K, group, terms, sms;
+    W4Plan plan;
+  };
+  static thread_local Entry kept[32];
+  const unsigned hash = ((unsigned)R * 2654435761u ^ (unsigned)N * 2246822519u ^ (unsigned)K * 3266489917u ^ (unsigned)(group + terms)) >> 27;
+  Entry& e = kept[hash];
+  if (e.R != R || e.N != N || e.K != K || e.group != group || e.terms != terms || e.sms != sms)
+    e = Entry{R, N, K, group, terms, sms, w4_plan(R, N, K, group, terms, sms)};
+  return e.plan;
+}
+
+template <int NT, int TERMS>
+static const void* w4_fn_ns(int group) {
+  if (group == 32) return (const void*)w4_gemv_kernel<NT, TERMS, 4>;
+  if (group == 64) return (const void*)w4_gemv_kernel<NT, TERMS, 2>;
+  return (const void*)w4_gemv_kernel<NT, TERMS, 1>;
+}
+template <int TERMS>
+static const void* w4_fn(int NT, int group) {
+  return NT == 1 ? w4_fn_ns<1, TERMS>(group) : (NT == 2 ? w4_fn_ns<2, TERMS>(group) : w4_fn_ns<4, TERMS>(group));
+}
 
 cudaError_t launch_w4_gemv(int R, int N, int K, int group, int xdt, int ydt, const void* x, long long xs, const void* packed,
                            void* y, long long ys, int sms, cudaStream_t s) {
   W4Gemv P{};
   P.x = x; P.w = static_cast<const unsigned char*>(packed); P.y = y;
   P.xs = xs; P.ys = ys;
-  P.R = R; P.N = N; P.K = K; P.group = group; P.xdt = xdt; P.ydt = ydt;
+  P.R = R; P.N = N; P.K = K; P.xdt = xdt; P.ydt = ydt;
   P.KB = (K + kW4TileK - 1) / kW4TileK;
-  P.XS = P.KB * 256 + 64;  // neighbouring columns half a bank row apart: a quarter warp's 16-byte reads meet no conflict
   P.xvec = xs * elem_bytes(xdt) % 16 == 0;
-  const int terms = xdt == kF32 ? 2 : 1;
-  // rows of x per CTA: as many as there are, up to 32 columns, that fit beside the rings
-  int rb = std::min(R, 32 / terms);
-  for (;; rb = (rb + 1) / 2) {
-    P.rb = rb;
-    P.wk = kW4Warps;
-    if (w4_smem(P, terms) <= kW4SmemMax) break;
-    if (rb == 1) return cudaErrorInvalidValue;
-  }
-  const int rblocks = (R + rb - 1) / rb;
-  P.rb = rb = (R + rblocks - 1) / rblocks;
-  const int cols = rb * terms, NT = cols <= 8 ? 1 : (cols <= 16 ? 2 : 4);
-  const int tiles = (N + 15) / 16;
-  // Warps that split K: the fewest that still give every resident CTA a group
-  // of tiles (no shares to add, no barrier), all eight when tiles are scarce.
-  const int regs_ctas = NT == 1 ? 3 : (NT == 2 ? 2 : 1);
-  int wk = 1, ctas = 1;
-  size_t smem = 0;
-  for (;; wk *= 2) {
-    P.wk = wk;
-    smem = w4_smem(P, terms);
-    ctas = (int)std::max<size_t>(1, std::min<size_t>(regs_ctas, kW4SmemMax / (smem + 1024)));
-    const int wm = kW4Warps / wk;
-    if (wk == kW4Warps || 2 * wk > P.KB || (long long)((tiles + wm - 1) / wm) * rblocks >= (long long)sms * ctas) break;
-  }
-  const int wm = kW4Warps / wk, groups = (tiles + wm - 1) / wm;
-  const int slots = std::max(1, sms * ctas / rblocks);
-  const int per = (groups + slots - 1) / slots;
-  const dim3 grid((groups + per - 1) / per, rblocks);
-  const void* fn = nullptr;
-  if (terms == 2) fn = NT == 1 ? (const void*)w4_gemv_kernel<1, 2> : (NT == 2 ? (const void*)w4_gemv_kernel<2, 2> : (const void*)w4_gemv_kernel<4, 2>);
-  else fn = NT == 1 ? (const void*)w4_gemv_kernel<1, 1> : (NT == 2 ? (const void*)w4_gemv_kernel<2, 1> : (const void*)w4_gemv_kernel<4, 1>);
+  const int terms = xdt == kF32 ? 2 : 1, tb = w4_tile_bytes(group);
+  const W4Plan plan = w4_plan_cached(R, N, K, group, terms, sms);
+  P.rb = plan.rb;
+  P.ck = plan.ck;
+  P.wk = plan.wk;
+  const size_t smem = w4_smem(P, terms, tb);
+  const int NT = w4_columns(P, terms);
+  const void* fn = terms == 2 ? w4_fn<2>(NT, group) : w4_fn<1>(NT, group);
   cudaError_t e = ops4_smem_limit(fn, smem);
   if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(plan.grid, (R + P.rb - 1) / P.rb);
+  cfg.blockDim = dim3(kW4Threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = P.ck;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = P.ck > 1 ? 1 : 0;
   void* args[] = {&P};
-  return cudaLaunchKernel(fn, grid, dim3(kW4Threads), args, smem, s);
+  return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 }  // namespace cpk_host

@@ -68,9 +68,9 @@ def test_kv4_refusals(lib):
         return lib.cp_spec_kv4_read(C.byref(shape), cache, pages, per, seqs, n, ln, dt, k, v, None)
 
     def attn(shape=ok, cache=A, pages=A, per=2, seqs=4, rows=3, nq=4, kl=A, nr=None, mask=None, scale=0.125, dt=0, q=A, qs=256,
-             o=A, os_=256, lse=None):
+             o=A, os_=256, lse=None, work=None, nbytes=0):
         return lib.cp_spec_kv4_attention(C.byref(shape), cache, pages, per, seqs, rows, nq, kl, nr, mask, scale, dt, q, qs, o,
-                                         os_, lse, None)
+                                         os_, lse, work, nbytes, None)
 
     shared = (dict(cache=None), dict(cache=OFF), dict(pages=OFF), dict(per=0), dict(per=1 << 28), dict(seqs=-1),
               dict(pages=None, per=3), dict(dt=3), dict(shape=_cache(b, page_size=8)))
@@ -79,7 +79,7 @@ def test_kv4_refusals(lib):
             assert f(**kw) == b.E_INVALID, (f.__name__, kw)
         assert f(shape=_cache(b, head_dim=80)) == b.E_UNSUPPORTED
         assert f(seqs=0) == b.OK
-        assert f(seqs=(1 << 31) - 1) == b.E_UNSUPPORTED  # 2^31 sequences x 2 pairs x 128 elements: above 2^38
+    assert append(rows=1 << 26) == read(n=1 << 26) == b.E_UNSUPPORTED  # 2^25 pairs of rows of 128 elements: above 2^32
     for kw in (dict(rows=-1), dict(pos=None), dict(pos=OFF), dict(nr=OFF), dict(k=None), dict(v=OFF), dict(ks=127), dict(vs=0)):
         assert append(**kw) == b.E_INVALID, kw
     assert append(rows=0) == b.OK
@@ -88,10 +88,14 @@ def test_kv4_refusals(lib):
     assert read(n=0) == b.OK
     for kw in (dict(nq=3), dict(nq=0), dict(nq=8192), dict(kl=None), dict(kl=OFF), dict(nr=OFF), dict(mask=OFF),
                dict(scale=float("nan")), dict(scale=float("inf")), dict(q=None), dict(q=OFF), dict(qs=255), dict(o=None),
-               dict(os_=255), dict(lse=OFF)):
+               dict(os_=255), dict(lse=OFF), dict(work=OFF)):
         assert attn(**kw) == b.E_INVALID, kw
-    assert attn(rows=65) == b.E_UNSUPPORTED
+    assert attn(rows=65) == attn(seqs=1 << 27) == b.E_UNSUPPORTED
     assert attn(rows=0) == b.OK
+    for bad in (dict(rows=65), dict(nq=3), dict(dt=3), dict(per=0), dict(seqs=0)):
+        d = dict(per=2, seqs=4, rows=3, nq=4, dt=0)
+        d.update(bad)
+        assert lib.cp_spec_kv4_attention_bytes(C.byref(ok), d["per"], d["seqs"], d["rows"], d["nq"], d["dt"]) == 0
 
 
 def test_binding_refuses_wrong_tensors(lib):
