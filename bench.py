@@ -106,7 +106,7 @@ def measured_peaks():
     return 6800.0, "fallback"
 
 
-PASS_KERNEL_SOURCES = ("cp_common.cuh", "cp_sampling.cuh", "cp_frame.cuh", "cp_t5.cuh", "cp_pass_kernels.cu")
+PASS_KERNEL_SOURCES = ("cp_common.cuh", "cp_sampling.cuh", "cp_frame.cuh", "cp_gemv.cuh", "cp_t5.cuh", "cp_pass_kernels.cu")
 
 
 def kernel_source_hash():

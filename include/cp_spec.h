@@ -233,6 +233,34 @@ cp_spec_status cp_spec_init_tree(const cp_spec_model* model, const cp_spec_weigh
                                  const cp_spec_config* config, const cp_spec_tree* tree, void* d_workspace,
                                  size_t workspace_bytes, cp_spec_ctx** out);
 
+/* Contexts over 4-bit weights.  The matrices (wq, wk, wv, wo, w_gate, w_up,
+ * w_down, lm_head) are given packed by cp_spec_w4_pack, each with groups of
+ * `group` along its rows; lm_head as one matrix [(G-1) * V][H].  embed stays in
+ * the model's dtype, the norms and draft offsets in float32.  Everything else
+ * is as for cp_spec_init (tree NULL) or cp_spec_init_tree: decoding, rounds,
+ * sampling, offsets, the adaptive window, counters (weight_bytes counts packed
+ * bytes).  The committed law is that of the decoder with the values that the
+ * packed weights stand for, computed in float32 (inputs count with 22 bits).
+ * kv_bits 32 keeps the float32 KV cache; 4 holds each stream's frame in a
+ * 4-bit cache (cp_spec_kv4_append, cp_spec_kv4_attention: one page per stream
+ * and layer) of 0.14 of its bytes, at the price of the keys' and values' own
+ * rounding; greedy codes of different windows may then differ where a value
+ * lies as close to a rounding border as float32 sums differ.  Made for few
+ * rows per pass: every block of 8 rows reads the weights again.
+ * Limits beside cp_spec_init's: head_dim a multiple of 32, vocab of 16; kv_bits
+ * 4 needs head_dim 64, 128 or 256 and chain rounds. */
+typedef struct {
+  int32_t group;   /* 32, 64 or 128 */
+  int32_t kv_bits; /* 32 or 4 */
+} cp_spec_quant;
+
+/* Workspace bytes of such a context (0 if the arguments are invalid). */
+size_t cp_spec_workspace_bytes_w4(const cp_spec_model* model, const cp_spec_config* config, const cp_spec_tree* tree,
+                                  const cp_spec_quant* quant);
+cp_spec_status cp_spec_init_w4(const cp_spec_model* model, const cp_spec_weights* weights, const cp_spec_config* config,
+                               const cp_spec_tree* tree, const cp_spec_quant* quant, void* d_workspace, size_t workspace_bytes,
+                               cp_spec_ctx** out);
+
 /* Per-stream sampling overrides, HOST arrays of n entries (n <= max_streams):
  * top_k in 1..config.top_k, temperature 0 (greedy) or in [1e-3, 100].
  * Synchronous (small host-to-device copy). */
@@ -471,6 +499,8 @@ cp_spec_status cp_spec_reset_stats(cp_spec_ctx* ctx, void* stream);
  *     ("Speculative Decoding, Beyond Text", section 07: the logical length
  *     and the valid-position mask).
  * 0 restores normal operation.  Nothing traps or spins without a bound.
+ * Packed weights have no bounded wait (bit 0) and a 4-bit cache no float slots
+ * (bit 1): CP_SPEC_E_UNSUPPORTED there.
  * Synchronises the device if the context's call graph exists (it is rebuilt
  * on the next call). */
 cp_spec_status cp_spec_test_hooks(cp_spec_ctx* ctx, uint64_t wait_limit_ns, int32_t flags);

@@ -28,7 +28,7 @@ EXPORTS = ("cp_spec_workspace_bytes", "cp_spec_init", "cp_spec_set_stream_sampli
            "cp_spec_last_error", "cp_spec_destroy", "cp_spec_decode_frames_static", "cp_spec_test_hooks",
            "cp_spec_workspace_bytes_tree", "cp_spec_init_tree", "cp_spec_w4_bytes", "cp_spec_w4_pack",
            "cp_spec_w4_unpack", "cp_spec_w4_gemv", "cp_spec_kv4_bytes", "cp_spec_kv4_append", "cp_spec_kv4_read",
-           "cp_spec_kv4_attention", "cp_spec_kv4_attention_bytes")
+           "cp_spec_kv4_attention", "cp_spec_kv4_attention_bytes", "cp_spec_workspace_bytes_w4", "cp_spec_init_w4")
 MAX_W4_K, MAX_KV4_ROWS = 32768, 64
 
 
@@ -58,6 +58,10 @@ class Config(C.Structure):
 
 class Tree(C.Structure):
     _fields_ = [("n", C.c_int32), ("parent", C.c_void_p), ("rank", C.c_void_p)]
+
+
+class Quant(C.Structure):
+    _fields_ = [("group", C.c_int32), ("kv_bits", C.c_int32)]
 
 
 class Kv4(C.Structure):
@@ -114,6 +118,9 @@ def load():
     L.cp_spec_kv4_attention.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, f32, i32, vp, i64, vp, i64, vp, vp, sz, vp]
     L.cp_spec_kv4_attention_bytes.argtypes = [vp, i32, i32, i32, i32, i32]
     L.cp_spec_kv4_attention_bytes.restype = sz
+    L.cp_spec_workspace_bytes_w4.argtypes = [vp, vp, vp, vp]
+    L.cp_spec_workspace_bytes_w4.restype = sz
+    L.cp_spec_init_w4.argtypes = [vp, vp, vp, vp, vp, vp, sz, C.POINTER(vp)]
     L.cp_spec_status_word.argtypes = [vp, vp]
     L.cp_spec_test_hooks.argtypes = [vp, u64, i32]
     L.cp_spec_read_stats.argtypes = [vp, vp, vp]
@@ -128,7 +135,7 @@ def load():
                  "cp_spec_round", "cp_spec_teacher_logits", "cp_spec_accept_batch", "cp_spec_status_word",
                  "cp_spec_read_stats", "cp_spec_reset_stats", "cp_spec_decode_frames_static", "cp_spec_test_hooks", "cp_spec_w4_pack",
                  "cp_spec_w4_unpack", "cp_spec_w4_gemv", "cp_spec_kv4_append", "cp_spec_kv4_read",
-                 "cp_spec_kv4_attention", "cp_spec_kv4_attention_bytes"):
+                 "cp_spec_kv4_attention", "cp_spec_kv4_attention_bytes", "cp_spec_workspace_bytes_w4", "cp_spec_init_w4"):
         getattr(L, name).restype = C.c_int
     _lib = L
     return L
@@ -142,7 +149,7 @@ def _check(rc: int, ctx=None, allow=(OK,)):
 
 
 def _ptr(t) -> int:
-    return 0 if t is None else int(t.data_ptr())
+    return 0 if t is None else int((t.data if isinstance(t, W4Matrix) else t).data_ptr())
 
 
 def _stream():
@@ -172,6 +179,14 @@ def weights_to_device(spec: synth.ModelSpec, w: dict, device="cuda") -> dict:
     return out
 
 
+def pack_weights(spec: synth.ModelSpec, dw: dict, group: int = 32) -> dict:
+    """Device weights with every matrix packed to 4 bits (W4Matrix), for CpSpec (cp_spec_init_w4)."""
+    out = dict(dw, w4_group=group)
+    out["lm_head"] = w4_pack(dw["lm_head"].view(-1, spec.hidden), group)
+    out["layers"] = [{k: v if k.endswith("norm") else w4_pack(v, group) for k, v in lw.items()} for lw in dw["layers"]]
+    return out
+
+
 def n_draft_offsets(dw: dict) -> int:
     """K of the position-aware draft offsets held in device weights (0 if none)."""
     off = dw.get("draft_offset")
@@ -193,9 +208,11 @@ class CpSpec:
 
     def __init__(self, spec: synth.ModelSpec, device_weights: dict, verify_window: int, top_k: int,
                  temperature: float, seed: int, max_streams: int = 1, adapt_pct: int = 0, adapt_min: int = 16,
-                 tree=None):
+                 tree=None, kv_bits: int = 32):
         """tree: None (chain rounds of verify_window), or (parent, rank) sequences of a sparse
-        draft tree (cp_spec_init_tree; verify_window and the adaptive window are then ignored)."""
+        draft tree (cp_spec_init_tree; verify_window and the adaptive window are then ignored).
+        device_weights from pack_weights make a context over 4-bit weights (cp_spec_init_w4), with
+        kv_bits = 4 its KV cache in 4 bits too."""
         import numpy as np
         import torch
         self.lib = load()
@@ -206,11 +223,20 @@ class CpSpec:
         self.config = Config(verify_window, top_k, temperature, seed, max_streams, n_draft_offsets(device_weights),
                              adapt_pct, adapt_min)
         self.tree = None
+        group = device_weights.get("w4_group")
+        self.quant = Quant(group, kv_bits) if group else None
+        if group is None and kv_bits != 32:
+            raise CpSpecError(E_INVALID, "a 4-bit KV cache needs packed weights (pack_weights)")
         if tree is not None:
             par = np.ascontiguousarray(tree[0], dtype=np.int32)
             rk = np.ascontiguousarray(tree[1], dtype=np.int32)
             self._tree_arrays = (par, rk)  # kept alive for the call
             self.tree = Tree(len(par), par.ctypes.data, rk.ctypes.data)
+        tree_ref = None if self.tree is None else C.byref(self.tree)
+        if self.quant is not None:
+            nbytes = self.lib.cp_spec_workspace_bytes_w4(C.byref(self.model), C.byref(self.config), tree_ref,
+                                                         C.byref(self.quant))
+        elif self.tree is not None:
             nbytes = self.lib.cp_spec_workspace_bytes_tree(C.byref(self.model), C.byref(self.config),
                                                            C.byref(self.tree))
         else:
@@ -219,7 +245,10 @@ class CpSpec:
             _check(E_INVALID)
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
         ctx = C.c_void_p()
-        if self.tree is not None:
+        if self.quant is not None:
+            rc = self.lib.cp_spec_init_w4(C.byref(self.model), C.byref(self.weights), C.byref(self.config), tree_ref,
+                                          C.byref(self.quant), C.c_void_p(_ptr(self.workspace)), nbytes, C.byref(ctx))
+        elif self.tree is not None:
             rc = self.lib.cp_spec_init_tree(C.byref(self.model), C.byref(self.weights), C.byref(self.config),
                                             C.byref(self.tree), C.c_void_p(_ptr(self.workspace)), nbytes,
                                             C.byref(ctx))

@@ -17,7 +17,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libcpspec.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["cp_spec.cu", "cp_pass_kernels.cu", "cp_accept_kernel.cu", "cp_w4.cu", "cp_kv4.cu"]
+SOURCES = ["cp_spec.cu", "cp_pass_kernels.cu", "cp_accept_kernel.cu", "cp_w4.cu", "cp_kv4.cu", "cp_w4_pass.cu"]
 
 
 def _nvcc() -> str:

@@ -138,6 +138,10 @@ struct FrameParams {
   int t5;           // bf16 GEMVs as tcgen05 tiles (contexts with many rows per pass)
   int t5_rb[5];     // ... pass rows per CTA tile, per GEMV kind (16, 32 or 64)
   int t5_stages[5]; // ... stages of the weight / input ring, per GEMV kind
+  int w4;           // packed 4-bit weights: elements per scale (0 = weights in `dtype`)
+  int w4_rb;        // ... pass rows per CTA
+  int w4_wk[5], w4_gx[5];  // ... warps that split K and CTAs along the tiles, per GEMV kind
+  int kv4;          // KV cache in 4 bits: page_size of a stream's page per layer (0 = float32 cache)
   const unsigned char* tmaps;  // ... TMA tensor maps of the weight matrices, 128 bytes each (t5_map_index)
   int test_stall;   // test hook: one bounded wait of the first GEMV of a pass never completes
   int test_poison;  // test hook: the accept kernel writes NaN into the KV slots the next pass must not read
@@ -147,6 +151,7 @@ struct FrameParams {
   unsigned long long seed;
   unsigned long long cond;            // graph conditional handle of the pass loop (0 = none)
   long long layer_bytes, head_bytes;  // algorithmic bytes per layer / per lm_head
+  long long kv_pos_bytes;             // ... and per KV position and layer
   const void* embed;
   const void* head;
   const float* final_norm;
@@ -165,7 +170,13 @@ struct FrameParams {
   float* qbuf;     // [Bmax*NS][nq*d]  queries after RoPE
   float* abuf;     // [Bmax*NS][nq*d]  attention outputs
   float* fbuf;     // [Bmax*NS][F]     SwiGLU activations
-  float* kv;       // [Bmax][L][2][G][nkv][d]
+  float* kv;       // [Bmax][L][2][G][nkv][d] (absent with a 4-bit cache)
+  unsigned char* kv4_cache;  // [L] caches of Bmax pages
+  size_t kv4_layer;          // bytes of one
+  float* kvrow;    // [2][Bmax*NS][nkv*d]  4-bit cache: the pass's keys (after RoPE) and values
+  int* kv4_pos;    // [Bmax] position of a stream's first row in the pass
+  int* kv4_rows;   // [Bmax] its rows in the pass
+  int* kv4_len;    // [Bmax] its positions, those rows among them
   float* logits;   // [Bmax*NS][1+ND][V]
   float* otab;     // [G-1][KO][V]     head_j . b_t, added to the lookahead-t draft logits
   int* lidx;       // [Bmax*NS][1+ND][KC]
@@ -215,15 +226,17 @@ inline __host__ __device__ size_t accept_scratch_bytes(int NSr, int NDr, int KC)
 // Workspace carve-up, computed identically by the host for sizing.
 struct Layout {
   size_t h, qbuf, abuf, fbuf, kv, logits, otab, lidx, lprob, lcount, qidx, qprob, qcount, row_pos, row_code, prow, ppos,
-      pcode, row_slot, pslot, ttok, tree, tmaps, plan, st, sstats, rope, top_k, temp, ctl, call, total;
+      pcode, row_slot, pslot, ttok, tree, tmaps, plan, st, sstats, rope, top_k, temp, ctl, call, kv4_cache, kvrow, kv4_pos, kv4_rows, kv4_len, total;
 };
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // NS row slots per stream, ND draft slots per row, GS KV slots per stream
 // and layer (chain rounds: NS = max(N, 2), ND = max(N - 1, 0), GS = G).
+// kv4_layer: bytes per layer of a 4-bit KV cache that takes the float cache's
+// place (0: none).
 inline Layout make_layout(int H, int L, int nq, int nkv, int d, int F, int V, int G, int NS, int ND, int GS, int KC,
-                          int Bmax, int KO) {
+                          int Bmax, int KO, size_t kv4_layer = 0) {
   const int NDq = ND > 0 ? ND : 1;
   const size_t rows = (size_t)Bmax * NS;
   Layout o{};
@@ -233,7 +246,7 @@ inline Layout make_layout(int H, int L, int nq, int nkv, int d, int F, int V, in
   o.qbuf = take(4 * rows * nq * d);
   o.abuf = take(4 * rows * nq * d);
   o.fbuf = take(4 * rows * F);
-  o.kv = take(4 * (size_t)Bmax * L * 2 * GS * nkv * d);
+  o.kv = take(kv4_layer ? 0 : 4 * (size_t)Bmax * L * 2 * GS * nkv * d);
   o.logits = take(4 * rows * (1 + ND) * V);
   o.otab = take(4 * (size_t)(G - 1) * KO * V);
   o.lidx = take(sizeof(int) * rows * (1 + ND) * KC);
@@ -260,6 +273,13 @@ inline Layout make_layout(int H, int L, int nq, int nkv, int d, int F, int V, in
   o.temp = take(sizeof(float) * (size_t)Bmax);
   o.ctl = take(sizeof(Control));
   o.call = take(sizeof(CallArgs));
+  if (kv4_layer) {
+    o.kv4_cache = take(kv4_layer * L);
+    o.kvrow = take(4 * 2 * rows * nkv * d);
+    o.kv4_pos = take(sizeof(int) * (size_t)Bmax);
+    o.kv4_rows = take(sizeof(int) * (size_t)Bmax);
+    o.kv4_len = take(sizeof(int) * (size_t)Bmax);
+  }
   o.total = off;
   return o;
 }

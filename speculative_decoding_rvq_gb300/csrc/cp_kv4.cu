@@ -925,7 +925,7 @@ static cudaError_t launch_attention(Kv4Attn& P, const Kv4Plan& L, int sms, cudaS
   const size_t smem = P.ring_at + (size_t)L.W * P.ring_stride;
   const void* fn = (const void*)kv4_attention_kernel<NG, NT, QT, PT>;
   cudaError_t e = ops4_smem_limit(fn, smem);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || P.q == nullptr) return e;  // (no queries: only readied)
   void* args[] = {&P};
   e = cudaLaunchKernel(fn, dim3((unsigned)(L.units * P.splits)), dim3(32 * L.W), args, smem, s);
   if (e != cudaSuccess || P.splits == 1) return e;
@@ -954,6 +954,16 @@ static cudaError_t launch_attention_types(Kv4Attn& P, const Kv4Plan& L, int sms,
   if (P.dtype == kF32) return launch_attention_nt<NG, 2, 2>(P, L, sms, s);
   if (P.dtype == kF16) return launch_attention_nt<NG, 1, 2>(P, L, sms, s);
   return launch_attention_nt<NG, 1, 1>(P, L, sms, s);
+}
+
+cudaError_t kv4_attention_configure(const Kv4Shape& S, int max_pages, int B, int M, int nq, int dtype) {
+  Kv4Attention A{};
+  A.max_pages = max_pages; A.B = B; A.M = M; A.nq = nq; A.dtype = dtype;
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, (const void*)kv4_append_kernel);  // (loads it)
+  for (int sms : {1, 1 << 16})  // (both ring depths)
+    if (e == cudaSuccess) e = launch_kv4_attention(S, A, sms, 0);
+  return e;
 }
 
 cudaError_t launch_kv4_attention(const Kv4Shape& S, const Kv4Attention& A, int sms, cudaStream_t s) {

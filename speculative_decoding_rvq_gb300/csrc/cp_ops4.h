@@ -42,6 +42,8 @@ struct Kv4Attention {
   void* work;  // kv4_attention_work bytes
 };
 size_t kv4_attention_work(const Kv4Shape& S, int max_pages, int B, int M, int nq, int dtype, int sms);
+// Readies the kernels of such a call on the current device, for a caller that captures its first one.
+cudaError_t kv4_attention_configure(const Kv4Shape& S, int max_pages, int B, int M, int nq, int dtype);
 cudaError_t launch_kv4_attention(const Kv4Shape& S, const Kv4Attention& A, int sms, cudaStream_t s);
 
 }  // namespace cpk_host

@@ -31,6 +31,8 @@ cudaError_t launch_init_tables(float2* rope, int G, int d, double theta, int* to
 cudaError_t launch_offset_table(const cpk::FrameParams& P, cudaStream_t stream);
 bool plan_mv(cpk::FrameParams& P, int sms);
 bool plan_t5(cpk::FrameParams& P, int sms);
+bool plan_w4(cpk::FrameParams& P, int sms);
+cudaError_t launch_offset_table_w4(const cpk::FrameParams& P, int sms, cudaStream_t stream);
 cudaError_t launch_accept_batch(int R, int N, int V, int k, float T, unsigned long long seed, int mode,
                                 const float* tgt, const float* drf, int* tokens, int* nacc, int* drafts,
                                 cudaStream_t stream);
@@ -146,11 +148,35 @@ Slots slots_for(const cp_spec_model* m, int N, const cpk::TreeTab* tree) {
   return Slots{N > 2 ? N : 2, N > 1 ? N - 1 : 0, m->num_code_groups};
 }
 
-cpk::Layout layout_for(const cp_spec_model* m, const cp_spec_config* cfg, int N, const cpk::TreeTab* tree = nullptr) {
+// A stream's page of a 4-bit cache: its G positions in whole tiles of 16.
+cpk_host::Kv4Shape frame_cache(const cp_spec_model* m, const cp_spec_config* cfg) {
+  return cpk_host::Kv4Shape{cfg->max_streams, (m->num_code_groups + 15) / 16 * 16, m->n_kv_heads, m->head_dim};
+}
+
+cpk::Layout layout_for(const cp_spec_model* m, const cp_spec_config* cfg, int N, const cpk::TreeTab* tree = nullptr,
+                       const cp_spec_quant* quant = nullptr) {
   const int KC = list_capacity(m, cfg);
   const Slots sl = slots_for(m, N, tree);
+  size_t kv4 = 0;
+  if (quant && quant->kv_bits == 4) {
+    const cpk_host::Kv4Shape S = frame_cache(m, cfg);
+    kv4 = cpk::align_up(cpk_host::kv4_bytes(S.n_pages, S.page_size, S.nkv, S.d), 256);
+  }
   return cpk::make_layout(m->hidden, m->n_layers, m->n_q_heads, m->n_kv_heads, m->head_dim, m->ffn, m->vocab,
-                          m->num_code_groups, sl.NS, sl.ND, sl.GS, KC, cfg->max_streams, offset_lookaheads(cfg, N));
+                          m->num_code_groups, sl.NS, sl.ND, sl.GS, KC, cfg->max_streams, offset_lookaheads(cfg, N), kv4);
+}
+
+// A context over packed weights: what the model has to fit beside cp_spec_init's limits.
+cp_spec_status check_quant(const cp_spec_model* m, const cp_spec_quant* q, const cp_spec_tree* tree) {
+  if (!q) return fail(nullptr, CP_SPEC_E_INVALID, "quant is null");
+  if (q->group != 32 && q->group != 64 && q->group != 128) return fail(nullptr, CP_SPEC_E_INVALID, "group must be 32, 64 or 128");
+  if (q->kv_bits != 32 && q->kv_bits != 4) return fail(nullptr, CP_SPEC_E_INVALID, "kv_bits must be 32 or 4");
+  if (m->head_dim % 32 || m->vocab % 16)
+    return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "packed weights need head_dim a multiple of 32 and vocab a multiple of 16");
+  if (q->kv_bits == 4 && (m->head_dim < 64 || (m->head_dim & (m->head_dim - 1))))
+    return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "a 4-bit KV cache needs head_dim 64, 128 or 256");
+  if (q->kv_bits == 4 && tree) return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "tree rounds move cache rows: they need the float cache");
+  return CP_SPEC_OK;
 }
 
 // Checks a sparse tree ("RVQ Position Aware Speculative Decoding for On
@@ -213,14 +239,18 @@ constexpr int kRedFloatsHost = 1536;                 // the GEMV kernel's partia
 constexpr int kRedQHost = 8;                         // its input-row stride
 constexpr int kTcMinRows = 32;                       // rows per pass (max_streams x row slots) that select the tensor path
 
-cp_spec_status check_shapes(const cp_spec_model* m, int N, int KC) {
+// `packed`: the GEMVs run over packed weights, whose kernel plans its own
+// shared memory (plan_w4).
+cp_spec_status check_shapes(const cp_spec_model* m, int N, int KC, bool packed) {
   const size_t eb = m->dtype == 1 ? 2 : 4;
   const int H = m->hidden, F = m->ffn, QD = m->n_q_heads * m->head_dim;
+  if (packed && std::max(std::max(H, QD), F) > CP_SPEC_MAX_W4_K)
+    return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "GEMV width above %d", CP_SPEC_MAX_W4_K);
   const size_t unit = std::max(std::max((size_t)2 * H, (size_t)QD), (size_t)F) * eb;
-  if (unit > (size_t)cpk::kSlotBytes)
+  if (!packed && unit > (size_t)cpk::kSlotBytes)
     return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "a weight row pair of %zu bytes exceeds the %d-byte tile", unit, cpk::kSlotBytes);
   const size_t maxk = (size_t)std::max(std::max(H, QD), F) * eb / 16;
-  if (maxk > (size_t)kMaxChunksPerRow)
+  if (!packed && maxk > (size_t)kMaxChunksPerRow)
     return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "GEMV width %zu bytes above %d", maxk * 16, kMaxChunksPerRow * 16);
   if (m->num_code_groups > 64 ||
       ((size_t)2 * m->num_code_groups * m->head_dim + (size_t)(m->n_q_heads / m->n_kv_heads) * m->head_dim + 4 * 64) * 4 >
@@ -230,7 +260,7 @@ cp_spec_status check_shapes(const cp_spec_model* m, int N, int KC) {
   // (the kernel's tile and row-group geometry, restated)
   const int Ks[4] = {H, QD, F, H};
   const int rpus[4] = {2, 1, 1, 1};
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4 && !packed; ++i) {
     const int nch = (int)((size_t)Ks[i] * eb / 16);
     const int TPG = std::min(cpk::kThreads, (nch + 31) / 32 * 32);
     const int WPG = TPG / 32;
@@ -251,13 +281,13 @@ struct DevicePlan {
 // Queries the current device and checks that the configuration fits the
 // pass kernels (shared memory of the top-k and accept kernels).
 cp_spec_status plan_device(const cp_spec_model* model, const cp_spec_config* config, int N, DevicePlan* dp,
-                           const cpk::TreeTab* tree = nullptr) {
+                           const cpk::TreeTab* tree = nullptr, bool packed = false) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return check_cuda(nullptr, e, "device query");
   const int KC = list_capacity(model, config);
-  cp_spec_status v = check_shapes(model, N, KC);
+  cp_spec_status v = check_shapes(model, N, KC, packed);
   if (v != CP_SPEC_OK) return v;
   const Slots sl = slots_for(model, N, tree);
   const int tn = tree ? tree->n : 0;
@@ -277,7 +307,7 @@ cp_spec_status plan_device(const cp_spec_model* model, const cp_spec_config* con
 // the carve-up of the workspace at `ws`.
 void fill_params(const cp_spec_model* model, const cp_spec_weights* weights, const cp_spec_config* config, int N,
                  const DevicePlan& dp, const cpk::Layout& lay, unsigned char* ws, cpk::FrameParams* out,
-                 const cpk::TreeTab* tree = nullptr) {
+                 const cpk::TreeTab* tree = nullptr, const cp_spec_quant* quant = nullptr) {
   cpk::FrameParams& P = *out;
   memset(&P, 0, sizeof P);
   const int L = model->n_layers;
@@ -297,11 +327,13 @@ void fill_params(const cp_spec_model* model, const cp_spec_weights* weights, con
   // bf16 contexts with many rows per pass run the GEMVs on tensor cores
   // (every GEMV width a multiple of 32); the choice depends on the context,
   // not on the pass, so a stream's results do not depend on its batch-mates
-  P.tc = (model->dtype == 1 && config->max_streams * NS >= kTcMinRows && model->hidden % 32 == 0 &&
+  P.w4 = quant ? quant->group : 0;
+  P.tc = (!P.w4 && model->dtype == 1 && config->max_streams * NS >= kTcMinRows && model->hidden % 32 == 0 &&
           model->ffn % 32 == 0 && (model->n_q_heads * model->head_dim) % 32 == 0) ? 1 : 0;
   P.mv = 0;
   P.t5 = 0;
-  if (!P.tc) cpk_host::plan_mv(P, dp.sms);  // bf16 contexts with at most 8 row slots
+  if (P.w4) P.w4_rb = 0;                    // planned below, once the shape is known to fit
+  else if (!P.tc) cpk_host::plan_mv(P, dp.sms);  // bf16 contexts with at most 8 row slots
   else cpk_host::plan_t5(P, dp.sms);        // tcgen05 tiles where the shape fits them
   P.wait_ns = cpk::kDefaultWaitNs;
   P.test_stall = 0;
@@ -313,6 +345,22 @@ void fill_params(const cp_spec_model* model, const cp_spec_weights* weights, con
                   kvd = (long long)model->n_kv_heads * model->head_dim, F = model->ffn;
   P.layer_bytes = (qd * H + 2 * kvd * H + H * qd + 3 * F * H) * eb + 2 * H * 4;
   P.head_bytes = (long long)model->vocab * H * eb;
+  P.kv_pos_bytes = 2 * kvd * 4;
+  if (P.w4) {
+    auto packed = [&](long long rows, long long k) { return (long long)cpk_host::w4_bytes((int)rows, (int)k, P.w4); };
+    P.layer_bytes = packed(qd, H) + 2 * packed(kvd, H) + packed(H, qd) + 2 * packed(F, H) + packed(H, F) + 2 * H * 4;
+    P.head_bytes = packed(model->vocab, H);
+  }
+  if (quant && quant->kv_bits == 4) {
+    const cpk_host::Kv4Shape S = frame_cache(model, config);
+    P.kv4 = S.page_size;
+    P.kv4_layer = cpk::align_up(cpk_host::kv4_bytes(S.n_pages, S.page_size, S.nkv, S.d), 256);
+    P.kv_pos_bytes = 2 * (kvd / 2 + kvd / 16);
+    P.kernels_per_pass = 6 * L + 3;
+    P.kv4_cache = at<unsigned char>(ws, lay.kv4_cache);
+    P.kvrow = at<float>(ws, lay.kvrow);
+    P.kv4_pos = at<int>(ws, lay.kv4_pos); P.kv4_rows = at<int>(ws, lay.kv4_rows); P.kv4_len = at<int>(ws, lay.kv4_len);
+  }
   P.embed = weights->embed; P.head = weights->lm_head; P.final_norm = weights->final_norm;
   for (int l = 0; l < L; ++l) {
     P.attn_norm[l] = weights->attn_norm[l]; P.wq[l] = weights->wq[l]; P.wk[l] = weights->wk[l];
@@ -493,13 +541,15 @@ namespace {
 
 // cp_spec_init, with a sparse tree (tree != null) or chain rounds.
 cp_spec_status init_impl(const cp_spec_model* model, const cp_spec_weights* weights, const cp_spec_config* config,
-                         const cp_spec_tree* tree_in, void* d_workspace, size_t workspace_bytes, cp_spec_ctx** out) {
+                         const cp_spec_tree* tree_in, void* d_workspace, size_t workspace_bytes, cp_spec_ctx** out,
+                         const cp_spec_quant* quant = nullptr) {
   if (!out) return fail(nullptr, CP_SPEC_E_INVALID, "out is null");
   *out = nullptr;
   cp_spec_status v = validate(model, config, nullptr);
   if (v != CP_SPEC_OK) return v;
   v = check_weights(model, config, weights);
   if (v != CP_SPEC_OK) return v;
+  if (quant && (v = check_quant(model, quant, tree_in)) != CP_SPEC_OK) return v;
   if (!d_workspace || !aligned16(d_workspace)) return fail(nullptr, CP_SPEC_E_INVALID, "workspace null or not 16-byte aligned");
   cpk::TreeTab tab;
   const cpk::TreeTab* tree = nullptr;
@@ -510,11 +560,11 @@ cp_spec_status init_impl(const cp_spec_model* model, const cp_spec_weights* weig
     tree = &tab;
   }
   const int N = tree ? tree->dmax + 1 : effective_window(model, config);
-  const cpk::Layout lay = layout_for(model, config, N, tree);
+  const cpk::Layout lay = layout_for(model, config, N, tree, quant);
   if (workspace_bytes < lay.total)
     return fail(nullptr, CP_SPEC_E_WORKSPACE, "workspace %zu bytes < required %zu", workspace_bytes, lay.total);
   DevicePlan dp;
-  v = plan_device(model, config, N, &dp, tree);
+  v = plan_device(model, config, N, &dp, tree, quant != nullptr);
   if (v != CP_SPEC_OK) return v;
 
   cp_spec_ctx* c = new (std::nothrow) cp_spec_ctx();
@@ -534,7 +584,11 @@ cp_spec_status init_impl(const cp_spec_model* model, const cp_spec_weights* weig
   c->staged = c->need_setup = false;
 
   cpk::FrameParams& P = c->base;
-  fill_params(model, weights, config, N, dp, lay, c->ws, &P, tree);
+  fill_params(model, weights, config, N, dp, lay, c->ws, &P, tree, quant);
+  if (P.w4 && !cpk_host::plan_w4(P, dp.sms)) {
+    delete c;
+    return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "a row of this model does not fit the packed GEMV's shared memory");
+  }
   std::vector<CUtensorMap> maps;
   if (P.t5 && !build_tmaps(P, &maps)) P.t5 = 0;  // no tensor maps: the tiles stay off
 
@@ -548,14 +602,15 @@ cp_spec_status init_impl(const cp_spec_model* model, const cp_spec_weights* weig
   if (e == cudaSuccess)
     e = cpk_host::launch_init_tables(P.rope, P.G, P.d, (double)model->rope_theta, P.top_k, P.temp, config->max_streams,
                                      config->top_k, config->temperature, 0);
-  if (e == cudaSuccess && P.KO > 0) e = cpk_host::launch_offset_table(P, 0);
+  if (e == cudaSuccess && P.KO > 0)
+    e = P.w4 ? cpk_host::launch_offset_table_w4(P, dp.sms, 0) : cpk_host::launch_offset_table(P, 0);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
     cp_spec_status s = check_cuda(nullptr, e, "workspace initialisation");
     delete c;
     return s;
   }
-  c->launches += P.KO > 0 ? 2 : 1;
+  c->launches += 1 + (P.KO > 0 ? (P.w4 ? P.G - 1 : 1) : 0);
   *out = c;
   if (!tree && N != window_of(config)) {
     c->err = "speculation disabled: fewer than 3 code groups leave no draft slot; running the autoregressive loop";
@@ -585,6 +640,21 @@ cp_spec_status cp_spec_init_tree(const cp_spec_model* model, const cp_spec_weigh
                                  size_t workspace_bytes, cp_spec_ctx** out) {
   if (!tree) return fail(nullptr, CP_SPEC_E_INVALID, "tree is null");
   return init_impl(model, weights, config, tree, d_workspace, workspace_bytes, out);
+}
+
+size_t cp_spec_workspace_bytes_w4(const cp_spec_model* model, const cp_spec_config* config, const cp_spec_tree* tree,
+                                  const cp_spec_quant* quant) {
+  if (validate(model, config, nullptr) != CP_SPEC_OK || check_quant(model, quant, tree) != CP_SPEC_OK) return 0;
+  cpk::TreeTab tab;
+  if (tree && build_tree(model, config, tree, &tab) != CP_SPEC_OK) return 0;
+  return layout_for(model, config, tree ? tab.dmax + 1 : effective_window(model, config), tree ? &tab : nullptr, quant).total;
+}
+
+cp_spec_status cp_spec_init_w4(const cp_spec_model* model, const cp_spec_weights* weights, const cp_spec_config* config,
+                               const cp_spec_tree* tree, const cp_spec_quant* quant, void* d_workspace, size_t workspace_bytes,
+                               cp_spec_ctx** out) {
+  if (!quant) return fail(nullptr, CP_SPEC_E_INVALID, "quant is null");
+  return init_impl(model, weights, config, tree, d_workspace, workspace_bytes, out, quant);
 }
 
 cp_spec_status cp_spec_set_stream_sampling(cp_spec_ctx* c, int32_t n, const int32_t* h_top_k, const float* h_temp) {
@@ -1035,6 +1105,8 @@ cp_spec_status cp_spec_test_hooks(cp_spec_ctx* c, uint64_t wait_limit_ns, int32_
   if (wait_limit_ns < 10000ull || wait_limit_ns > 60ull * 1000000000ull)
     return fail(c, CP_SPEC_E_INVALID, "wait_limit_ns must be in [1e4, 6e10]");
   if (flags < 0 || flags > 3) return fail(c, CP_SPEC_E_INVALID, "flags must be in [0, 3]");
+  if ((c->base.w4 && (flags & 1)) || (c->base.kv4 && (flags & 2)))
+    return fail(c, CP_SPEC_E_UNSUPPORTED, "packed weights have no bounded wait to stall, a 4-bit cache no float slots to poison");
   // the parameter block is part of the call graph: drop the graph (rebuilt on the next call)
   if (c->graph) {
     cudaError_t e = cudaDeviceSynchronize();

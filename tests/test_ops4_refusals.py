@@ -137,3 +137,26 @@ def test_binding_refuses_wrong_tensors(lib):
     for bad in ((0, 16, 2, 64), (8, 20, 2, 64), (8, 16, 2, 72)):
         with pytest.raises(b.CpSpecError):
             b.Kv4Cache(*bad, device="cpu")
+
+
+def test_w4_context_sizes_and_refusals(lib):
+    from speculative_decoding_rvq_gb300 import binding as b, synth as S
+    m = b.model_struct(S.TINY_FP32)
+    cfg = b.Config(4, 50, 0.9, 1, 2)
+    size = lambda model=m, group=32, bits=32: lib.cp_spec_workspace_bytes_w4(C.byref(model), C.byref(cfg), None,
+                                                                             C.byref(b.Quant(group, bits)))
+    assert size() == lib.cp_spec_workspace_bytes(C.byref(m), C.byref(cfg))
+    assert 0 < size(bits=4) < size()
+    for bad in (dict(group=16), dict(group=0), dict(bits=8), dict(bits=0)):
+        assert size(**bad) == 0, bad
+    for d, v in ((48, 256), (64, 250)):
+        other = b.model_struct(S.ModelSpec(256, 2, 4, 4, d, 768, v, 8, 0))
+        assert size(model=other) == 0
+    narrow = b.model_struct(S.ModelSpec(256, 2, 4, 4, 32, 768, 256, 8, 0))
+    assert size(model=narrow) > 0 and size(model=narrow, bits=4) == 0
+    ctx = C.c_void_p()
+    w = b.Weights()
+    q = b.Quant(32, 32)
+    assert lib.cp_spec_init_w4(C.byref(m), C.byref(w), C.byref(cfg), None, None, A, 1 << 30, C.byref(ctx)) == b.E_INVALID
+    assert lib.cp_spec_init_w4(C.byref(m), C.byref(w), C.byref(cfg), None, C.byref(q), A, 1 << 30, C.byref(ctx)) == b.E_INVALID
+    assert lib.cp_spec_init_w4(C.byref(m), None, C.byref(cfg), None, C.byref(q), A, 1 << 30, C.byref(ctx)) == b.E_INVALID
