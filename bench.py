@@ -258,6 +258,7 @@ def run_gpu(args, rank, world):
         result["batched"] = batched(spec, dw, peak)
         result["draft_offsets"] = offsets_line(spec, dw, xd[:200], cd[:200], peak)
         result["sparse_tree"] = tree_line(spec, dw, xd[:200], cd[:200], peak)
+        result["packed_weights"] = packed_line(spec, dw, xd[:200], cd[:200], peak)
         if not args.no_large:
             result["large"] = large_line(peak)
     return result
@@ -363,6 +364,36 @@ def tree_line(spec, dw, xd, cd, peak):
                      "passes_per_frame": round(st["passes"] / F, 3), "us_per_pass": round(ms * 1e3 / st["passes"], 2),
                      "codes_per_round": round((F * (G - 2)) / max(st["rounds"], 1), 3),
                      "accepted_by_depth": st["accepted_by_offset"][1:4],
+                     "hbm_frac": round((st["weight_bytes"] + st["kv_bytes"]) / (ms / 1e3) / 1e9 / peak, 4)}
+        cp.close()
+    return out
+
+
+def packed_line(spec, dw, xd, cd, peak):
+    """The frames of xd (1 stream), top-k 50, T 0.9, over 4-bit weights (scales per 32), the AR loop and N = 4, with
+    the float32 KV cache and with the 4-bit one."""
+    import torch
+    from speculative_decoding_rvq_gb300 import binding
+    packed = binding.pack_weights(spec, dw, 32)
+    G, F = spec.num_code_groups, xd.shape[0]
+    out = {"frames": int(F), "group": 32}
+    for name, N, bits in (("AR", 0, 32), ("N4", 4, 32), ("N4_kv4", 4, 4)):
+        cp = binding.CpSpec(spec, packed, N, TOP_K, TEMP, SEED, 1, kv_bits=bits)
+        codes = torch.empty((F, 1, G), dtype=torch.int32, device="cuda")
+        cp.decode_frames(xd[:4], cd[:4], codes[:4])
+        torch.cuda.synchronize()
+        cp.reset_stats()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        cp.decode_frames(xd, cd, codes)
+        b.record()
+        torch.cuda.synchronize()
+        cp.status()
+        ms = a.elapsed_time(b)
+        st = cp.stats()
+        out[name] = {"codes_per_s": round(F * (G - 1) / (ms / 1e3), 1), "passes_per_frame": round(st["passes"] / F, 3),
+                     "us_per_pass": round(ms * 1e3 / st["passes"], 2),
+                     "weight_mb_per_pass": round(st["weight_bytes"] / st["passes"] / 1e6, 1),
                      "hbm_frac": round((st["weight_bytes"] + st["kv_bytes"]) / (ms / 1e3) / 1e9 / peak, 4)}
         cp.close()
     return out
