@@ -49,7 +49,7 @@ __device__ __forceinline__ int kv4_page(const Kv4Map& M, int b, int at) {
 }
 
 __device__ __forceinline__ unsigned char* kv4_tile(const Kv4Map& M, int page, int h, int tile_in_page) {
-  return M.cache + page * M.page_stride + (h * M.tpp + tile_in_page) * kv4_tile_bytes(M.d);
+  return M.cache + page * M.page_stride + (long long)(h * M.tpp + tile_in_page) * kv4_tile_bytes(M.d);  // (a page may pass 2^31 bytes)
 }
 
 // ------------------------------------------------------------ write, read

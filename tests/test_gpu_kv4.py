@@ -344,6 +344,32 @@ def test_offsets_beyond_32_bits(b):
     _against_64(b, cache, pages, k, v, _randn(9, 2, 2, 8, 128, dtype=torch.bfloat16), [200, 150])
 
 
+def test_offsets_within_a_page_beyond_32_bits(b):
+    """Pages of 2.4 GB: the last head's slots lie past 2^31 bytes of their page."""
+    for nkv, d, page, first in ((1024, 64, 1 << 15, 0), (8, 256, 1 << 20, 131072 - 7)):
+        cache = b.Kv4Cache(1, page, nkv, d)
+        assert cache.data.numel() > 1 << 31
+        k, v = _randn(1, 1, 20, nkv, d, dtype=torch.bfloat16), _randn(2, 1, 20, nkv, d, dtype=torch.bfloat16)
+        cache.append(k, v, _int([first]))
+        # the same memory as pages of one tile of one head: the last head's first tiles with these rows
+        tiles = page // 16
+        small = b.Kv4Cache(1, 16, 1, d)
+        small.shape.n_pages = small.n_pages = nkv * tiles
+        small.data = cache.data
+        t0 = first // 16
+        table = _int([[(nkv - 1) * tiles + t0 + j for j in range(3)]])
+        skip = first - 16 * t0
+        gk, gv = small.read(skip + 20, pages=table)
+        for got, want in ((gk, hold(k, 32)), (gv, hold(v, 32))):
+            assert torch.equal(got[0, skip:, 0].double(), want[0, :, -1]) and (got[0, :skip] == 0).all()
+        gk, gv = cache.read(first + 20, dtype=torch.bfloat16)
+        for got, want in ((gk, hold(k, 32)), (gv, hold(v, 32))):
+            assert torch.equal(got[:, first:], want.float().to(torch.bfloat16)) and not got[:, :first].any()
+        del gk, gv
+        if first == 0:
+            _against_64(b, cache, _int([[0]]), k, v, _randn(9, 1, 2, nkv, d, dtype=torch.bfloat16), [20])
+
+
 def test_same_results_again_captured_and_on_another_stream(b):
     """Long enough to be split over CTAs; lengths and queries change between the replays of one graph."""
     cache, pages, k, v = _filled(b, 2, 4000, 2, 128, 64, "bf16", seed=4)
