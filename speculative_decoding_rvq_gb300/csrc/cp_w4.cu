@@ -300,12 +300,16 @@ cudaError_t ops4_smem_limit(const void* fn, size_t bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(mu);
-  size_t& h = high[std::make_pair(dev, fn)];
-  if (bytes <= h) return cudaSuccess;
-  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) h = bytes;
-  return e;
+  try {  // (nothing is thrown across the C entry)
+    std::lock_guard<std::mutex> lock(mu);
+    size_t& h = high[std::make_pair(dev, fn)];
+    if (bytes <= h) return cudaSuccess;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) h = bytes;
+    return e;
+  } catch (...) {
+    return cudaErrorMemoryAllocation;
+  }
 }
 
 size_t w4_bytes(int N, int K, int group) {
