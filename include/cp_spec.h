@@ -331,9 +331,10 @@ cp_spec_status cp_spec_accept_batch(int32_t R, int32_t N, int32_t V, int32_t top
  *
  * The format.  A value is s * c, with c one of the sixteen E2M1 numbers +-0,
  * 0.5, 1, 1.5, 2, 3, 4, 6 and s the bfloat16 scale of a group of consecutive
- * elements: s = bf16(max |x| / 6), c the E2M1 number nearest to x / s, ties to
- * the even code, saturating at 6.  A group that holds an infinity or a NaN
- * reads back as NaN; one whose scale rounds to zero reads back as zeros.
+ * elements: s = bf16(max |x| * r), r the float32 number nearest to 1/6, c the
+ * E2M1 number nearest to x / s, ties to the even code, saturating at 6.  A
+ * group that holds an infinity or a NaN reads back as NaN; one whose scale
+ * rounds to zero reads back as zeros.
  *
  * Element types (dtype, out_dtype): 0 float32, 1 bfloat16, 2 float16.  Row
  * strides count elements; a row itself is dense. */

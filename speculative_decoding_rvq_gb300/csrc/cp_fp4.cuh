@@ -2,9 +2,11 @@
 // 4-bit operators share.
 //
 // A value is s * c with c one of the sixteen E2M1 numbers (+-0, 0.5, 1, 1.5,
-// 2, 3, 4, 6) and s the bfloat16 scale of its group.  s = bf16(max |x| / 6),
-// both roundings to nearest even; c is the E2M1 number nearest to x / s, ties
-// to the even code.  The float32 quotient decides like the exact one: a tie
+// 2, 3, 4, 6) and s the bfloat16 scale of its group.  s = bf16(max |x| * r), r
+// the float32 number nearest to 1/6, the product rounded to float32 and then to
+// bfloat16, both to nearest even (for bfloat16 and fp16 inputs the same as
+// max |x| / 6; for float32 inputs 1.5 groups in a million get the neighbouring
+// scale); c is the E2M1 number nearest to x / s, ties to the even code.  The float32 quotient decides like the exact one: a tie
 // point is s times a number of at most three bits, hence a float32 number,
 // and for any other x the quotient differs from the tie point by more than
 // half an ulp.  A group that holds an infinity or a NaN gets a NaN scale (all
@@ -50,11 +52,13 @@ __device__ __forceinline__ uint32_t float2_to_e2m1(float lo, float hi) {
   return r;
 }
 
+constexpr float kSixth = 0x1.555556p-3f;  // 1/6 rounded to float32
+
 // Bits of the scale of a group whose largest finite magnitude is amax;
 // `bad`: the group holds an infinity or a NaN.
 __device__ __forceinline__ uint32_t fp4_scale_bits(float amax, bool bad) {
   if (bad) return 0x7FC0u;
-  return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(amax, 6.0f)));
+  return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(amax, kSixth)));
 }
 __device__ __forceinline__ float bf16_bits_f32(uint32_t b) { return __uint_as_float(b << 16); }
 

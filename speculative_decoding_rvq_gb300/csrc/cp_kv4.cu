@@ -75,7 +75,7 @@ struct Kv4Rows {
   bool kvec, vvec;
 };
 
-// a / b for b = 6 or a scale of ordinary size, correctly rounded, from the
+// a / b for a scale b of ordinary size, correctly rounded, from the
 // correctly rounded reciprocal y of b: q = a y, then q + (a - q b) y with fused
 // multiply-adds (Markstein, "Computation of elementary functions on the IBM
 // RISC System/6000 processor", 1990).
@@ -113,7 +113,7 @@ __device__ __forceinline__ uint32_t kv4_scaled(const uint32_t (&raw)[8], int dty
                                    : (dtype == kBF16 ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top)));
   uint32_t bits;
   if (amax > 0x1p-90f && amax < 0x1p100f) {  // (false for what is not finite)
-    bits = __bfloat16_as_ushort(__float2bfloat16_rn(quotient_by(amax, 6.0f, 0x1.555556p-3f)));
+    bits = __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(amax, kSixth)));
     const float s = bf16_bits_f32(bits), y = __frcp_rn(s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = quotient_by(q[i], s, y);

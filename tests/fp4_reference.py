@@ -13,6 +13,10 @@ HALF_TINY = {t: torch.finfo(t).smallest_normal * torch.finfo(t).eps / 2 for t in
 # (measured: addends below 2^-24 of the largest are lost): at most 17 such losses per step.
 MMA_STEP = 17 * 2.0 ** -24
 
+# the float32 number nearest to 1/6: a group's scale is bf16(float32(largest magnitude * SIXTH)); a product of two float32
+# numbers is exact in float64, so .float() is its one rounding
+SIXTH = float.fromhex("0x1.555556p-3")
+
 
 def hold(x, group):
     """float64 values that the format holds for x [..., width], groups along the last axis."""
@@ -22,7 +26,7 @@ def hold(x, group):
     x = x.view(*x.shape[:-1], x.shape[-1] // group, group)
     finite = torch.isfinite(x).all(-1, keepdim=True)
     x = torch.where(finite, x, torch.zeros_like(x))
-    s = (x.abs().amax(-1, keepdim=True) / 6.0).float().bfloat16().double()
+    s = (x.abs().amax(-1, keepdim=True) * SIXTH).float().bfloat16().double()
     r = (x / torch.where(s > 0, s, torch.ones_like(s))).abs()
     mid = (table[1:] + table[:-1]) / 2
     lo, hi = torch.bucketize(r, mid), torch.bucketize(r, mid, right=True)

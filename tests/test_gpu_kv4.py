@@ -62,6 +62,22 @@ def test_rows_read_back_as_the_held_values(b, nkv, d, page, dtype, rows, first):
                 assert (got[i, :p] == 0).all() and (got[i, p + rows:] == 0).all()
 
 
+def test_scales_between_two_bfloat16_numbers(b):
+    """Largest magnitudes whose sixth lies within a float32 step of the middle of two bfloat16 numbers: the scale is the
+    rounded product with float32(1/6) in the cache and in a packed matrix."""
+    top = [float.fromhex(h) for h in ("0x1.907ffep+1", "0x1.c07ffep+1", "0x1.c67ffep+1", "0x1.cc7ffep+1")]
+    x = torch.zeros(1, 16, 1, 64, device="cuda")
+    for i, t in enumerate(top):
+        for j in range(4):
+            x[0, 4 * i + j, 0, 5], x[0, 4 * i + j, 0, 40] = t * 2.0 ** (j - 2), -t * 2.0 ** j
+            x[0, 4 * i + j, 0, 20] = 1.5 * 2.0 ** (j - 2)
+    cache = b.Kv4Cache(1, 16, 1, 64)
+    cache.append(x, -x, _int([0]))
+    k, v = cache.read(16)
+    assert torch.equal(k.double(), hold(x, 32)) and torch.equal(v.double(), hold(-x, 32))
+    assert torch.equal(b.w4_unpack(b.w4_pack(x[0, :, 0], 32)).double(), hold(x[0, :, 0], 32))
+
+
 def test_values_that_are_not_finite_read_back_as_nan(b):
     cache = b.Kv4Cache(1, 16, 1, 64)
     k, v = _randn(1, 1, 4, 1, 64), _randn(2, 1, 4, 1, 64)

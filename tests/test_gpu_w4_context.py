@@ -9,7 +9,7 @@ import math
 import numpy as np
 import pytest
 
-from fp4_reference import hold
+from fp4_reference import SIXTH, hold
 from gpu_common import compare_codes_with_margins, require_gpu, torch
 
 pytestmark = pytest.mark.gpu
@@ -155,7 +155,7 @@ def test_benchmark_shapes(orc):
 def _border(x):
     """Smallest distance of a group's quotients x / s from a point between two held numbers, relative."""
     x = x.double().unflatten(-1, (-1, 32))
-    s = (x.abs().amax(-1, keepdim=True) / 6.0).float().bfloat16().double()
+    s = (x.abs().amax(-1, keepdim=True) * SIXTH).float().bfloat16().double()
     r = (x / s).abs().unsqueeze(-1)
     mid = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=torch.float64, device=x.device)
     return float(((r - mid).abs() / mid).min())
