@@ -420,7 +420,12 @@ cp_spec_status cp_spec_kv4_read(const cp_spec_kv4* shape, const void* d_cache, c
  * e / (n_q_heads / n_kv_heads).  d_lse (optional, out) [n_seqs][rows][n_q_heads]
  * float32: the log of the sum of the exponentials.  A row that sees nothing
  * gives zeros and -infinity; a position that a row does not see cannot reach it,
- * whatever is stored there.  Rows at or past d_rows[b] are left as they were.
+ * whatever is stored there, not by a bit.  Rows at or past d_rows[b] are left as
+ * they were.  Scores and sums are float32 (float32 queries count with 22 bits); a
+ * weight times a value's scale counts with 11 bits (bfloat16) or 22 (float16,
+ * float32), and with a weight of 1 standing for the row's largest never finer
+ * than 2^-31 of the largest value scale that the row sees in any channel of the
+ * head: channels or positions far smaller than that lose bits.
  * Results do not depend on timing or on the other sequences' contents, but
  * max_pages and the numbers of sequences, heads and rows choose how a long
  * sequence is split, which moves them within rounding.

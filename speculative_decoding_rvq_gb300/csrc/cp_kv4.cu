@@ -320,10 +320,12 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ K
 // for the few query rows of decoding (rows as M would waste 8 to 15 of 16).
 //
 // Precision.  q: fp16 with a power of two per row (bfloat16 and fp16 exactly,
-// float32 as hi + lo, QT = 2).  p * scale: fp16 brought to at most 2^15 by
-// a power of two that follows the largest scale seen, so it keeps eleven bits
-// down to 2^-29 of the largest product; fp16 and float32 outputs take the
-// rest as a second term (PT = 2), since one term would add about as much error
+// float32 as hi + lo, QT = 2).  p * scale: fp16 under a power of two per column
+// that brings the largest scale S which the column has seen, in any group of the
+// head, to [2^6, 2^7) at weight 1 (p <= 256 then stays in range): eleven bits
+// down to 2^-20 of S, below that an error of at most 2^-31 of S; fp16 and float32
+// outputs take the rest as a second term (PT = 2: 22 bits down to 2^-9 of S, the
+// same 2^-31 below), since one term would add about as much error
 // as fp16's own rounding.  The sum of p is float32.  Float32 outputs are added
 // up outside the tensor core, whose accumulation truncates (QT = 2).
 //
@@ -549,12 +551,16 @@ __global__ void __launch_bounds__(32 * kKvMaxWarps, kv4_ctas(NG, NT)) kv4_attent
   // Per column: the reference m (log2 units), the score above which it moves
   // (in raw score units), and what is taken from a score: m less the power of
   // two that brings the values' scales to [2^6, 2^7), so that it costs nothing
-  // to apply.  l and O carry that power; it is taken out at the end.
+  // to apply.  l and O carry that power; it is taken out at the end.  All of
+  // them follow from the positions that the column sees and from nothing else:
+  // a position that it does not see changes no bit of it.
   float O[NG][2][NT][4], mref[NT][2], thr[NT][2], sub[NT][2], l[NT][2];
+  uint32_t ecol[NT];  // biased exponents of the largest value scales that the two columns have seen, 16 bits each
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) { mref[n][c] = thr[n][c] = -INFINITY; l[n][c] = sub[n][c] = 0.0f; }
+    ecol[n] = E0 * 0x10001u;
 #pragma unroll
     for (int w = 0; w < NG; ++w)
 #pragma unroll
@@ -562,7 +568,7 @@ __global__ void __launch_bounds__(32 * kKvMaxWarps, kv4_ctas(NG, NT)) kv4_attent
 #pragma unroll
         for (int c = 0; c < 4; ++c) O[w][u][n][c] = 0.0f;
   }
-  uint32_t ecur = E0;  // biased exponent of the largest value scale seen
+  uint32_t emin = E0;  // the smallest of this lane's columns' exponents
 
   int stage = 0;
 #pragma unroll 1
@@ -630,7 +636,7 @@ __global__ void __launch_bounds__(32 * kKvMaxWarps, kv4_ctas(NG, NT)) kv4_attent
       }
     }
 
-    // does the reference have to move?
+    // does a reference, or a power of two, have to move?
     bool move = false;
     uint32_t top2 = 0;
 #pragma unroll
@@ -643,32 +649,45 @@ __global__ void __launch_bounds__(32 * kKvMaxWarps, kv4_ctas(NG, NT)) kv4_attent
 #pragma unroll
       for (int c = 0; c < 2; ++c)
         move |= fmaxf(fmaxf(fmaxf(sc[0][n][c], sc[0][n][2 + c]), sc[1][n][c]), sc[1][n][2 + c]) > thr[n][c];
-    if (__any_sync(0xffffffffu, move || (max(top2 & 0xFFFFu, top2 >> 16) >> 7) > ecur)) {
-      uint32_t e = 0;  // the largest exponent of a finite scale
+    if (__any_sync(0xffffffffu, move || (max(top2 & 0xFFFFu, top2 >> 16) >> 7) > emin)) {
+      uint32_t e[2][2];  // the largest exponent of a token's finite scales
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
+        for (int hh = 0; hh < 2; ++hh) {
+          e[s][hh] = 0;
 #pragma unroll
           for (int w = 0; w < NG; ++w) {
             const uint32_t x = (vs[s][hh][w >> 1] >> (16 * (w & 1)) & 0xFFFFu) >> 7;
-            if (x < 255u) e = max(e, x);
+            if (x < 255u) e[s][hh] = max(e[s][hh], x);
           }
-      const uint32_t enew = max(ecur, __reduce_max_sync(0xffffffffu, e));
-      const float er = pow2_of_biased(max(127 + (int)ecur - (int)enew, 0));
-      ecur = enew;
+        }
+      emin = 255u;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) {
+        uint32_t seen = 0;  // the largest of the tokens that a column sees, for both columns
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh)
+            seen = __vmaxu2(seen, (sc[s][n][2 * hh] == -INFINITY ? 0u : e[s][hh]) |
+                                      (sc[s][n][2 * hh + 1] == -INFINITY ? 0u : e[s][hh] << 16));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) seen = __vmaxu2(seen, __shfl_xor_sync(0xffffffffu, seen, o));
+        const uint32_t enew = __vmaxu2(seen, ecol[n]);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float mx = fmaxf(fmaxf(sc[0][n][c], sc[0][n][2 + c]), fmaxf(sc[1][n][c], sc[1][n][2 + c])) * fac[n][c];
+          float mx = fmaxf(fmaxf(sc[0][n][c], sc[0][n][2 + c]), fmaxf(sc[1][n][c], sc[1][n][2 + c]));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          mx = fmaxf(mx, mref[n][c]);
-          const float al = (mx == mref[n][c] ? 1.0f : ex2(mref[n][c] - mx)) * er;
+          // (a column moves for its own scores only, not because another one does)
+          mx = mx > thr[n][c] ? fmaxf(mx * fac[n][c], mref[n][c]) : mref[n][c];
+          const int e0 = ecol[n] >> (16 * c) & 0xFFFFu, e1 = enew >> (16 * c) & 0xFFFFu;
+          const float al = (mx == mref[n][c] ? 1.0f : ex2(mref[n][c] - mx)) * pow2_of_biased(max(127 + e0 - e1, 0));
           mref[n][c] = mx;
           thr[n][c] = __fdiv_rn(mx + 8.0f, fac[n][c]);
-          sub[n][c] = mx == -INFINITY ? 0.0f : mx - (float)(6 + 127 - (int)ecur);
+          sub[n][c] = mx == -INFINITY ? 0.0f : mx - (float)(6 + 127 - e1);
+          emin = min(emin, (uint32_t)e1);
           l[n][c] *= al;
 #pragma unroll
           for (int w = 0; w < NG; ++w)
@@ -678,6 +697,8 @@ __global__ void __launch_bounds__(32 * kKvMaxWarps, kv4_ctas(NG, NT)) kv4_attent
               O[w][u][n][2 + c] *= al;
             }
         }
+        ecol[n] = enew;
+      }
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -768,11 +789,11 @@ __global__ void __launch_bounds__(32 * kKvMaxWarps, kv4_ctas(NG, NT)) kv4_attent
   // the warps' shares through shared memory (each over its own ring)
   {
     float* mo = reinterpret_cast<float*>(ring);  // [C][RS]
-    const float back = pow2_of_biased((int)ecur - 6);  // 2^(ecur - 127 - 6)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
+        const float back = pow2_of_biased((int)(ecol[n] >> (16 * c) & 0xFFFFu) - 6);  // 2^(exponent - 127 - 6)
         float s = l[n][c];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);

@@ -1,0 +1,72 @@
+"""What attention over the 4-bit cache does with positions that a row does not see, and with values that are not finite
+in positions that it does see but weighs with zero."""
+import pytest
+
+from fp4_reference import DTYPES
+from gpu_common import require_gpu, torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+@pytest.fixture(scope="module")
+def b():
+    from speculative_decoding_rvq_gb300 import binding
+    return binding
+
+
+def _randn(seed, *shape, dtype=torch.float32, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (scale * torch.randn(*shape, generator=g, device="cuda")).to(dtype)
+
+
+def _int(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _largest(dtype, size):
+    return min(size, float(torch.finfo(DTYPES[dtype]).max))
+
+
+@pytest.mark.parametrize("size", [1e6, 1e10, 1e30, float("inf")])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("m,nq,nkv,d,lens", [
+    (4, 16, 8, 128, [4, 16, 21]),      # frames: one tile holds prefix and window
+    (6, 4, 2, 64, [6, 500, 37]),       # two column tiles
+    (24, 4, 1, 128, [40, 24, 1300]),   # four column tiles (16-bit types), several row tiles
+    (8, 2, 1, 256, [8, 90, 700])])
+def test_what_a_row_does_not_see_changes_no_bit(b, m, nq, nkv, d, lens, dtype, tree, size):
+    """One row of the window becomes large (or NaN): the outputs and the sums of every row that does not see it keep
+    every bit, by causal order and by a mask."""
+    seqs, spoilt = len(lens), m // 2
+    per = -(-max(lens) // 16)
+    cache = b.Kv4Cache(seqs * per, 16, nkv, d)
+    pages = torch.randperm(seqs * per, generator=torch.Generator().manual_seed(m)).to(torch.int32).view(seqs, per).cuda()
+    k, v = (_randn(i, seqs, max(lens), nkv, d, dtype=DTYPES[dtype]) for i in (1, 2))
+    cache.append(k, v, _int([0] * seqs), pages=pages, n_rows=_int(lens))
+    q = _randn(3, seqs, m, nq, d, dtype=DTYPES[dtype], scale=2.0)
+    # row i of the mask sees itself and the rows of its own parity before it: half of the rows do not see `spoilt`
+    rows = [sum(1 << j for j in range(i + 1) if (i - j) % 2 == 0) for i in range(m)]
+    mask = torch.tensor([rows] * seqs, dtype=torch.int64, device="cuda") if tree else None
+    kv_len = _int(lens)
+    clean, lse = cache.attention(q, kv_len, pages=pages, mask=mask, want_lse=True)
+    assert torch.isfinite(clean).all() and torch.isfinite(lse).all()
+    bad = _largest(dtype, size) * _randn(4, seqs, 1, nkv, d).sign()
+    if size == float("inf"):
+        bad = torch.full_like(bad, float("nan"))
+    bad = bad.to(DTYPES[dtype])
+    cache.append(bad, bad, kv_len - m + spoilt, pages=pages)
+    got, got_lse = cache.attention(q, kv_len, pages=pages, mask=mask, want_lse=True)
+    changed = 0
+    for i in range(m):
+        if rows[i] >> spoilt & 1 if tree else i >= spoilt:
+            changed += int((got[:, i] != clean[:, i]).any())
+        else:
+            assert torch.equal(got[:, i], clean[:, i]), (i, float((got[:, i].float() - clean[:, i].float()).abs().max()))
+            assert torch.equal(got_lse[:, i], lse[:, i]), i
+    assert changed
