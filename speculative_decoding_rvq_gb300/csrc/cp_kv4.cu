@@ -586,6 +586,7 @@ __global__ void __launch_bounds__(32 * kKvMaxWarps, kv4_ctas(NG, NT)) kv4_attent
 
     float sc[2][NT][4];
     uint32_t vs[2][2][NG / 2];
+    uint32_t hidden = 0;  // bit ((2 s + hh) NT + n) 2 + c: column c of n-tile n does not see token g + 8 hh of tile s
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const unsigned char* T = st + s * TB;
@@ -630,7 +631,10 @@ __global__ void __launch_bounds__(32 * kKvMaxWarps, kv4_ctas(NG, NT)) kv4_attent
             for (int c = 0; c < 2; ++c) {
               const int col = n * 8 + 2 * t + c;
               const bool see = there && (j < 0 || (P.mask ? (s_mask[col] >> j) & 1ull : (unsigned long long)(j <= s_row[col])));
-              if (!see) sc[s][n][2 * hh + c] = -INFINITY;
+              if (!see) {
+                sc[s][n][2 * hh + c] = -INFINITY;
+                hidden |= 1u << (((2 * s + hh) * NT + n) * 2 + c);
+              }
             }
         }
       }
@@ -710,8 +714,9 @@ __global__ void __launch_bounds__(32 * kKvMaxWarps, kv4_ctas(NG, NT)) kv4_attent
           l[n][c & 1] += sc[s][n][c];
         }
 
-    // O^T += V^T P^T.  KEEP: some weights are masked, and a masked token adds
-    // nothing whatever its scale is.
+    // O^T += V^T P^T.  KEEP: some tokens are hidden, and a hidden token adds
+    // nothing whatever its scale is.  (A token that is seen and whose weight
+    // underflows to zero still brings a NaN of its values, as in any other tile.)
     auto values = [&](auto keep_tag) {
       constexpr bool KEEP = decltype(keep_tag)::value;
       uint32_t keep[2][2][NT];
@@ -721,8 +726,10 @@ __global__ void __launch_bounds__(32 * kKvMaxWarps, kv4_ctas(NG, NT)) kv4_attent
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
-              keep[s][hh][n] = (sc[s][n][2 * hh] == 0.0f ? 0u : 0x0000FFFFu) | (sc[s][n][2 * hh + 1] == 0.0f ? 0u : 0xFFFF0000u);
+            for (int hh = 0; hh < 2; ++hh) {
+              const uint32_t two = hidden >> (((2 * s + hh) * NT + n) * 2);
+              keep[s][hh][n] = (two & 1u ? 0u : 0x0000FFFFu) | (two & 2u ? 0u : 0xFFFF0000u);
+            }
       }
       uint32_t va[2][NG], vb[2][NG];
 #pragma unroll

@@ -70,3 +70,23 @@ def test_what_a_row_does_not_see_changes_no_bit(b, m, nq, nkv, d, lens, dtype, t
             assert torch.equal(got[:, i], clean[:, i]), (i, float((got[:, i].float() - clean[:, i].float()).abs().max()))
             assert torch.equal(got_lse[:, i], lse[:, i]), i
     assert changed
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("at", [3, 20, 34, 37])
+def test_a_value_weighed_with_zero_still_counts(b, at, dtype):
+    """softmax(s) v with a NaN in v is NaN wherever the row sees it, however small its weight: the same in the prefix (3,
+    20), in a tile that the window shares (34) and in the window (37), where rows before it do not see it."""
+    n, m, nkv, d = 40, 4, 2, 64
+    cache = b.Kv4Cache(3, 16, nkv, d)
+    k, v = torch.zeros(1, n, nkv, d, device="cuda"), _randn(2, 1, n, nkv, d)
+    k[0, 1], k[0, at], v[0, at, :, 40] = 1.0, -10.0, float("nan")
+    q = torch.full((1, m, 4, d), 10.0, device="cuda")  # scores of 80, 0 and -800: weights of 1, 2e-35 and 0
+    cache.append(k.to(DTYPES[dtype]), v.to(DTYPES[dtype]), _int([0]))
+    o = cache.attention(q.to(DTYPES[dtype]), _int([n]))
+    for i in range(m):
+        assert torch.isfinite(o[0, i, :, :32]).all()
+        if at <= n - m + i:
+            assert torch.isnan(o[0, i, :, 32:]).all(), i
+        else:
+            assert torch.isfinite(o[0, i]).all(), i
