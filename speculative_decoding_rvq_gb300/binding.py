@@ -149,7 +149,7 @@ def _check(rc: int, ctx=None, allow=(OK,)):
 
 
 def _ptr(t) -> int:
-    return 0 if t is None else int((t.data if isinstance(t, W4Matrix) else t).data_ptr())
+    return 0 if t is None else int(t.data_ptr())
 
 
 def _stream():
@@ -193,12 +193,19 @@ def n_draft_offsets(dw: dict) -> int:
     return 0 if off is None else int(off.shape[0])
 
 
-def weights_struct(dw: dict) -> Weights:
+def weights_struct(dw: dict, packed: bool = False) -> Weights:
+    """The pointers of device weights; packed: every matrix but embed is a W4Matrix (cp_spec_init_w4), else none is."""
+    def matrix(m):
+        if isinstance(m, W4Matrix) != packed:
+            raise CpSpecError(E_INVALID, "plain matrices among packed weights" if packed else
+                              "packed 4-bit matrices where plain ones are wanted")
+        return _ptr(m.data if packed else m)
+
     ws = Weights()
-    ws.embed, ws.lm_head, ws.final_norm = _ptr(dw["embed"]), _ptr(dw["lm_head"]), _ptr(dw["final_norm"])
+    ws.embed, ws.lm_head, ws.final_norm = _ptr(dw["embed"]), matrix(dw["lm_head"]), _ptr(dw["final_norm"])
     for l, lw in enumerate(dw["layers"]):
         for n in ("attn_norm", "wq", "wk", "wv", "wo", "ffn_norm", "w_gate", "w_up", "w_down"):
-            getattr(ws, n)[l] = _ptr(lw[n])
+            getattr(ws, n)[l] = _ptr(lw[n]) if n.endswith("norm") else matrix(lw[n])
     ws.draft_offset = _ptr(dw.get("draft_offset"))
     return ws
 
@@ -219,7 +226,7 @@ class CpSpec:
         self.spec = spec
         self.dw = device_weights
         self.model = model_struct(spec)
-        self.weights = weights_struct(device_weights)
+        self.weights = weights_struct(device_weights, packed=bool(device_weights.get("w4_group")))
         self.config = Config(verify_window, top_k, temperature, seed, max_streams, n_draft_offsets(device_weights),
                              adapt_pct, adapt_min)
         self.tree = None
@@ -342,18 +349,18 @@ def accept_batch(target, draft, top_k: int, temperature: float, seed: int, mode:
 def decode_frames_static(spec: synth.ModelSpec, device_weights: dict, verify_window: int, top_k: int,
                          temperature: float, seed: int, x, c0, codes=None, first_frame: int = 0, max_streams=None,
                          status=None):
-    """cp_spec_decode_frames_static: one decode in the library's static scratch, no context.
+    """cp_spec_decode_frames_static: one decode in the library's static scratch, no context (no packed weights).
 
     x [F, B, H] float32 cuda, c0 [F, B] int32 cuda -> codes [F, B, G] int32 (asynchronous).
     status (optional) is a 1-element int32 cuda tensor that receives the device status word.
     Returns (codes, rc) with rc OK or W_AR_FALLBACK."""
     import torch
+    weights = weights_struct(device_weights)
     lib = load()
     F, B, _ = x.shape
     if codes is None:
         codes = torch.empty((F, B, spec.num_code_groups), dtype=torch.int32, device=x.device)
     model = model_struct(spec)
-    weights = weights_struct(device_weights)
     config = Config(verify_window, top_k, temperature, seed, B if max_streams is None else max_streams,
                     n_draft_offsets(device_weights))
     rc = lib.cp_spec_decode_frames_static(C.byref(model), C.byref(weights), C.byref(config), B, F, first_frame,

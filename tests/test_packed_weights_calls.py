@@ -1,0 +1,63 @@
+"""Packed weights reach the calls that take them and no other, with the shapes and groups that the call names (no GPU
+needed: the library is replaced by a recorder that nothing may reach)."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from speculative_decoding_rvq_gb300 import binding as b, synth as S
+
+SPEC = S.TINY_FP32
+
+
+@pytest.fixture
+def no_library(monkeypatch):
+    class Untouched:
+        def __getattr__(self, name):
+            raise AssertionError(f"the binding reached {name}")
+    monkeypatch.setattr(b, "load", lambda: Untouched())
+
+
+def _matrix(n, k, group, rows=None):
+    return b.W4Matrix(n, k, group, torch.zeros(16, dtype=torch.uint8))
+
+
+def _packed(group=32):
+    """Weights as pack_weights returns them, with empty codes."""
+    s, qd, kvd = SPEC, SPEC.n_q_heads * SPEC.head_dim, SPEC.n_kv_heads * SPEC.head_dim
+    shapes = dict(wq=(qd, s.hidden), wk=(kvd, s.hidden), wv=(kvd, s.hidden), wo=(s.hidden, qd), w_gate=(s.ffn, s.hidden),
+                  w_up=(s.ffn, s.hidden), w_down=(s.hidden, s.ffn))
+    norm = torch.ones(s.hidden)
+    layers = [dict({k: _matrix(*v, group) for k, v in shapes.items()}, attn_norm=norm, ffn_norm=norm)
+              for _ in range(s.n_layers)]
+    return dict(w4_group=group, embed=torch.zeros(s.num_code_groups - 1, s.vocab, s.hidden), final_norm=norm,
+                lm_head=_matrix((s.num_code_groups - 1) * s.vocab, s.hidden, group), layers=layers)
+
+
+def _refused(f):
+    with pytest.raises(b.CpSpecError) as e:
+        f()
+    assert e.value.code == b.E_INVALID, e.value
+    return str(e.value)
+
+
+def test_decode_without_a_context_refuses_packed_weights(no_library):
+    x, c0 = torch.zeros(1, 1, SPEC.hidden), torch.zeros(1, 1, dtype=torch.int32)
+    assert "packed" in _refused(lambda: b.decode_frames_static(SPEC, _packed(), 4, 50, 0.9, 1, x, c0))
+    w = _packed()
+    del w["w4_group"]  # (the matrices alone say it too)
+    _refused(lambda: b.decode_frames_static(SPEC, w, 4, 50, 0.9, 1, x, c0))
+
+
+def test_contexts_refuse_mixed_weights(no_library):
+    """A plain matrix among packed ones, and packed ones without their group."""
+    spec = (4, 50, 0.9, 1)
+    for name in ("wq", "w_down"):
+        w = _packed()
+        w["layers"][-1][name] = torch.zeros(w["layers"][-1][name].n, SPEC.hidden)
+        _refused(lambda: b.CpSpec(SPEC, w, *spec))
+    w = _packed()
+    w["lm_head"] = torch.zeros(SPEC.num_code_groups - 1, SPEC.vocab, SPEC.hidden)
+    _refused(lambda: b.CpSpec(SPEC, w, *spec))
+    w = _packed()
+    del w["w4_group"]
+    _refused(lambda: b.CpSpec(SPEC, w, *spec))
