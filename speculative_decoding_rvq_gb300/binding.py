@@ -210,6 +210,20 @@ def weights_struct(dw: dict, packed: bool = False) -> Weights:
     return ws
 
 
+def _check_packed(spec: synth.ModelSpec, dw: dict, group: int):
+    """Refuses packed matrices that do not have the model's shapes, the context's group and all their bytes."""
+    H, F, qd, kvd = spec.hidden, spec.ffn, spec.n_q_heads * spec.head_dim, spec.n_kv_heads * spec.head_dim
+    shapes = {"wq": (qd, H), "wk": (kvd, H), "wv": (kvd, H), "wo": (H, qd), "w_gate": (F, H), "w_up": (F, H), "w_down": (H, F)}
+    named = [("lm_head", dw["lm_head"], ((spec.num_code_groups - 1) * spec.vocab, H))]
+    named += [(f"layer {l} {n}", lw[n], shape) for l, lw in enumerate(dw["layers"]) for n, shape in shapes.items()]
+    for name, m, (n, k) in named:
+        if (m.n, m.k, m.group) != (n, k, group):
+            raise CpSpecError(E_INVALID, f"{name}: [{m.n}, {m.k}] in groups of {m.group}, [{n}, {k}] in groups of {group} wanted")
+    for name, m, _ in named:
+        if m.data.numel() < load().cp_spec_w4_bytes(m.n, m.k, m.group):
+            raise CpSpecError(E_INVALID, f"{name}: fewer bytes than a packed matrix of its shape has")
+
+
 class CpSpec:
     """One context of the CUDA library over device-resident weights."""
 
@@ -232,6 +246,8 @@ class CpSpec:
         self.tree = None
         group = device_weights.get("w4_group")
         self.quant = Quant(group, kv_bits) if group else None
+        if group:
+            _check_packed(spec, device_weights, group)
         if group is None and kv_bits != 32:
             raise CpSpecError(E_INVALID, "a 4-bit KV cache needs packed weights (pack_weights)")
         if tree is not None:

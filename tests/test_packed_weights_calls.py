@@ -61,3 +61,26 @@ def test_contexts_refuse_mixed_weights(no_library):
     w = _packed()
     del w["w4_group"]
     _refused(lambda: b.CpSpec(SPEC, w, *spec))
+
+
+@pytest.mark.parametrize("name", ["wq", "wk", "wv", "wo", "w_gate", "w_up", "w_down", "lm_head"])
+def test_contexts_refuse_other_shapes_and_groups(no_library, name):
+    """Each matrix has the model's rows and columns and the one group that the context is made for."""
+    for change in (dict(n=16), dict(n=-16), dict(k=128), dict(k=-128), dict(group=64)):
+        w = _packed()
+        at = w if name == "lm_head" else w["layers"][-1]
+        m = at[name]
+        at[name] = _matrix(m.n + change.get("n", 0), m.k + change.get("k", 0), change.get("group", m.group))
+        assert name in _refused(lambda: b.CpSpec(SPEC, w, 4, 50, 0.9, 1)), change
+    w = _packed(32)
+    w["w4_group"] = 128  # matrices packed with groups of 32
+    _refused(lambda: b.CpSpec(SPEC, w, 4, 50, 0.9, 1))
+
+
+def test_contexts_refuse_short_matrices(monkeypatch):
+    """Fewer bytes than a packed matrix of that shape has."""
+    class Sizes:
+        def cp_spec_w4_bytes(self, n, k, group):
+            return (n + 15) // 16 * ((k + 127) // 128) * (1024 + 32 * (128 // group))
+    monkeypatch.setattr(b, "load", lambda: Sizes())
+    assert "bytes" in _refused(lambda: b.CpSpec(SPEC, _packed(), 4, 50, 0.9, 1))
