@@ -384,7 +384,7 @@ typedef struct {
   int32_t n_pages, page_size, n_kv_heads, head_dim;
 } cp_spec_kv4;
 
-/* Bytes of the cache, 0 if the shape is invalid. */
+/* Bytes of the cache, 0 if the shape is invalid or the cache would pass 2^48 bytes. */
 size_t cp_spec_kv4_bytes(const cp_spec_kv4* shape);
 
 /* Quantises rows of keys and values as they are written: row i of sequence b

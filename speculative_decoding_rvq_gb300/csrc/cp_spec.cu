@@ -819,6 +819,9 @@ cp_spec_status check_kv4(const cp_spec_kv4* S) {
     return fail(nullptr, CP_SPEC_E_INVALID, "page_size must be a multiple of 16 in [16, 2^20]");
   if (S->head_dim != 64 && S->head_dim != 128 && S->head_dim != 256)
     return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "head_dim must be 64, 128 or 256");
+  // (a page is below 2^39 bytes by the limits above; offsets are formed in 64 bits)
+  if ((size_t)S->n_pages > (size_t(1) << 48) / cpk_host::kv4_bytes(1, S->page_size, S->n_kv_heads, S->head_dim))
+    return fail(nullptr, CP_SPEC_E_UNSUPPORTED, "the cache must not exceed 2^48 bytes");
   return CP_SPEC_OK;
 }
 
