@@ -135,7 +135,7 @@ def load():
                  "cp_spec_round", "cp_spec_teacher_logits", "cp_spec_accept_batch", "cp_spec_status_word",
                  "cp_spec_read_stats", "cp_spec_reset_stats", "cp_spec_decode_frames_static", "cp_spec_test_hooks", "cp_spec_w4_pack",
                  "cp_spec_w4_unpack", "cp_spec_w4_gemv", "cp_spec_kv4_append", "cp_spec_kv4_read",
-                 "cp_spec_kv4_attention", "cp_spec_kv4_attention_bytes", "cp_spec_workspace_bytes_w4", "cp_spec_init_w4"):
+                 "cp_spec_kv4_attention", "cp_spec_init_w4"):
         getattr(L, name).restype = C.c_int
     _lib = L
     return L

@@ -29,3 +29,15 @@ def test_a_cache_whose_size_passes_64_bits_is_refused(lib):
     assert lib.cp_spec_kv4_attention(C.byref(huge), A, A, 1, 0, 1, 1024, A, None, None, 1.0, 0, A, 1 << 18, A, 1 << 18, None,
                                      None, 0, None) == b.E_UNSUPPORTED
     assert lib.cp_spec_kv4_attention_bytes(C.byref(huge), 1, 1, 1, 1024, 0) == 0
+
+
+def test_sizes_above_two_gigabytes_come_back_whole(lib):
+    """A context over packed weights with many streams: its workspace passes 2^31 and 2^32 bytes, as the plain one's does."""
+    from speculative_decoding_rvq_gb300 import binding as b, synth as S
+    m = b.model_struct(S.TTS06B_BF16)
+    for streams in (256, 512, 1024, 2048, 4096):
+        cfg = b.Config(8, 50, 0.9, 1, streams)
+        plain = lib.cp_spec_workspace_bytes(C.byref(m), C.byref(cfg))
+        assert lib.cp_spec_workspace_bytes_w4(C.byref(m), C.byref(cfg), None, C.byref(b.Quant(32, 32))) == plain
+        assert 0 < lib.cp_spec_workspace_bytes_w4(C.byref(m), C.byref(cfg), None, C.byref(b.Quant(32, 4))) < plain
+    assert plain > 1 << 32
