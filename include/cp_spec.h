@@ -518,8 +518,9 @@ cp_spec_status cp_spec_test_hooks(cp_spec_ctx* ctx, uint64_t wait_limit_ns, int3
  * count in a process-wide counter, ctx = NULL. */
 int64_t cp_spec_launch_count(const cp_spec_ctx* ctx);
 
-/* Last error message of the context (or of the last context-free call when
- * ctx is NULL).  Never NULL. */
+/* Last error message of the context, or (ctx NULL) of the last call without a
+ * context that the calling thread made and that was refused; valid until that
+ * thread's next refused call.  Never NULL. */
 const char* cp_spec_last_error(const cp_spec_ctx* ctx);
 
 /* Release the host context.  Does not touch the caller's device memory. */

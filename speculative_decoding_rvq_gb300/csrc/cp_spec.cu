@@ -61,7 +61,7 @@ struct cp_spec_ctx {
 
 namespace {
 
-std::string g_err = "";
+thread_local char g_err[512];  // message of the thread's last refused call without a context
 std::atomic<long long> g_free_launches{0};
 
 cp_spec_status fail(cp_spec_ctx* c, cp_spec_status s, const char* fmt, ...) {
@@ -70,7 +70,7 @@ cp_spec_status fail(cp_spec_ctx* c, cp_spec_status s, const char* fmt, ...) {
   va_start(ap, fmt);
   vsnprintf(buf, sizeof buf, fmt, ap);
   va_end(ap);
-  if (c) c->err = buf; else g_err = buf;
+  if (c) c->err = buf; else strcpy(g_err, buf);
   return s;
 }
 
@@ -1127,7 +1127,7 @@ int64_t cp_spec_launch_count(const cp_spec_ctx* c) {
   return c ? c->launches : g_free_launches.load();
 }
 
-const char* cp_spec_last_error(const cp_spec_ctx* c) { return c ? c->err.c_str() : g_err.c_str(); }
+const char* cp_spec_last_error(const cp_spec_ctx* c) { return c ? c->err.c_str() : g_err; }
 
 void cp_spec_destroy(cp_spec_ctx* c) {
   if (!c) return;
