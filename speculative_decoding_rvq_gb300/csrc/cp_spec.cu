@@ -794,12 +794,12 @@ cudaError_t device_sms(int* sms) {
   return e;
 }
 
-cp_spec_status launched(cudaError_t e, const char* what) {
+cp_spec_status launched(cudaError_t e, const char* what, int kernels = 1) {
   if (e != cudaSuccess) {
     cudaGetLastError();  // a refused launch is reported here and nowhere else
     return check_cuda(nullptr, e, what);
   }
-  g_free_launches.fetch_add(1);
+  g_free_launches.fetch_add(kernels);
   return CP_SPEC_OK;
 }
 
@@ -982,7 +982,7 @@ cp_spec_status cp_spec_kv4_attention(const cp_spec_kv4* shape, const void* d_cac
   if (need > (d_work ? work_bytes : 0))
     return fail(nullptr, CP_SPEC_E_WORKSPACE, "needs %zu bytes of workspace (cp_spec_kv4_attention_bytes)", need);
   return launched(cpk_host::launch_kv4_attention(kv4_shape(shape), A, sms, static_cast<cudaStream_t>(stream)),
-                  "kv4 attention launch");
+                  "kv4 attention launch", need ? 2 : 1);  // (a split sequence's shares are joined by a second kernel)
 }
 
 cp_spec_status cp_spec_decode_frames_static(const cp_spec_model* model, const cp_spec_weights* weights,
