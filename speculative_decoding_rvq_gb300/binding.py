@@ -420,13 +420,23 @@ def _stream_on(dev: int) -> int:
     return _torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _index(t, n: int, what: str, dev: int) -> int:
+def _aligned(t, keep: list) -> int:
+    """Pointer of a dense tensor; a slice that does not start on 16 bytes is copied, the copy kept for the call."""
+    at = t.data_ptr()
+    if at & 15:
+        t = t.clone()
+        keep.append(t)
+        at = t.data_ptr()
+    return at
+
+
+def _index(t, n: int, what: str, dev: int, keep: list) -> int:
     """Pointer of a dense int32 tensor of n elements on device dev, or 0 for None."""
     if t is None:
         return 0
     if t.dtype is not _torch.int32 or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
         _refuse(f"{what}: {n} dense int32 values beside the cache wanted")
-    return t.data_ptr()
+    return _aligned(t, keep)
 
 
 def _row_stride(t, what: str) -> int:
@@ -502,7 +512,8 @@ class Kv4Cache:
     """Keys and values held in 4 bits, in n_pages pages of page_size token slots.
 
     pages (int32 [n_seqs, max_pages]) maps the positions of each sequence to pages; without it
-    sequence b owns n_pages // n_seqs neighbouring pages.  The memory starts as zeros."""
+    sequence b owns n_pages // n_seqs neighbouring pages.  The memory starts as zeros.  Slices of tables,
+    positions, lengths and masks may start anywhere; rows of keys, values and queries start on 16 bytes."""
 
     def __init__(self, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, device="cuda"):
         lib = _fast()
@@ -514,13 +525,13 @@ class Kv4Cache:
         self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = n_pages, page_size, n_kv_heads, head_dim
         self.data = _torch.zeros(nbytes, dtype=_torch.uint8, device=device)
 
-    def _pages(self, pages, n_seqs: int, dev: int):
+    def _pages(self, pages, n_seqs: int, dev: int, keep: list):
         """Pointer of the page table and pages per sequence."""
         if pages is None:
             return 0, self.n_pages // max(n_seqs, 1)
         if pages.dim() != 2 or pages.shape[0] != n_seqs:
             _refuse(f"pages: [{n_seqs}, max_pages] wanted")
-        return _index(pages, pages.numel(), "pages", dev), pages.shape[1]
+        return _index(pages, pages.numel(), "pages", dev, keep), pages.shape[1]
 
     def append(self, k, v, pos, pages=None, n_rows=None):
         """Write rows k, v [n_seqs, rows, n_kv_heads, head_dim]: row i of sequence b at position pos[b] + i (i < n_rows[b])."""
@@ -531,9 +542,10 @@ class Kv4Cache:
             _refuse(f"k, v: [n_seqs, rows, {self.n_kv_heads}, {self.head_dim}] of one type beside the cache wanted")
         b = shape[0]
         code, stream = _elem_type(dt), _stream_on(dev)
-        table, per = self._pages(pages, b, dev)
-        rc = lib.cp_spec_kv4_append(self._shape, data.data_ptr(), table, per, b, shape[1], _index(pos, b, "pos", dev),
-                                    _index(n_rows, b, "n_rows", dev), code, k.data_ptr(), _row_stride(k, "k"), v.data_ptr(),
+        keep = []
+        table, per = self._pages(pages, b, dev, keep)
+        rc = lib.cp_spec_kv4_append(self._shape, data.data_ptr(), table, per, b, shape[1], _index(pos, b, "pos", dev, keep),
+                                    _index(n_rows, b, "n_rows", dev, keep), code, k.data_ptr(), _row_stride(k, "k"), v.data_ptr(),
                                     _row_stride(v, "v"), stream)
         if rc:
             _check(rc)
@@ -546,11 +558,12 @@ class Kv4Cache:
         dev = data.get_device()
         stream = _stream_on(dev)
         b = n_seqs if n_seqs is not None else (pages.shape[0] if pages is not None else 1)
-        table, per = self._pages(pages, b, dev)
+        keep = []
+        table, per = self._pages(pages, b, dev, keep)
         dtype = dtype or _torch.float32
         size, code = (b, length, self.n_kv_heads, self.head_dim), _elem_type(dtype)
         k, v = _torch.empty(size, dtype=dtype, device=data.device), _torch.empty(size, dtype=dtype, device=data.device)
-        rc = lib.cp_spec_kv4_read(self._shape, data.data_ptr(), table, per, b, length, _index(lens, b, "lens", dev), code,
+        rc = lib.cp_spec_kv4_read(self._shape, data.data_ptr(), table, per, b, length, _index(lens, b, "lens", dev, keep), code,
                                   k.data_ptr(), v.data_ptr(), stream)
         if rc:
             _check(rc)
@@ -575,18 +588,18 @@ class Kv4Cache:
             if out.shape != shape or out.dtype is not dt or out.get_device() != dev:
                 _refuse("out: q's shape, type and device wanted")
             os = _row_stride(out, "out")
-        bits = 0
+        bits, keep = 0, []
         if mask is not None:
             if (mask.dtype is not _torch.int64 or tuple(mask.shape) != (b, m) or not mask.is_contiguous()
                     or mask.get_device() != dev):
                 _refuse(f"mask: dense int64 [{b}, {m}] wanted")
-            bits = mask.data_ptr()
+            bits = _aligned(mask, keep)
         lse = _torch.empty((b, m, nq), dtype=_torch.float32, device=data.device) if want_lse else None
-        table, per = self._pages(pages, b, dev)
+        table, per = self._pages(pages, b, dev, keep)
         need = lib.cp_spec_kv4_attention_bytes(self._shape, per, b, m, nq, code)
         work = _torch.empty(need, dtype=_torch.uint8, device=data.device) if need else None  # (freed in stream order)
-        rc = lib.cp_spec_kv4_attention(self._shape, data.data_ptr(), table, per, b, m, nq, _index(kv_len, b, "kv_len", dev),
-                                       _index(n_rows, b, "n_rows", dev), bits, d ** -0.5 if scale is None else scale, code,
+        rc = lib.cp_spec_kv4_attention(self._shape, data.data_ptr(), table, per, b, m, nq, _index(kv_len, b, "kv_len", dev, keep),
+                                       _index(n_rows, b, "n_rows", dev, keep), bits, d ** -0.5 if scale is None else scale, code,
                                        q.data_ptr(), _row_stride(q, "q"), out.data_ptr(), os,
                                        lse.data_ptr() if want_lse else 0, work.data_ptr() if need else 0, need, stream)
         if rc:

@@ -47,3 +47,39 @@ def test_the_launch_count_is_that_of_the_kernels(b):
     per = lib.cp_spec_kv4_attention_bytes(cache._shape, 512, 1, 2, 4, 0)
     assert per > 0  # a table of 8192 positions is split
     assert count(lambda: cache.attention(q, lens)) == 2
+
+
+def test_tables_lengths_and_masks_may_be_slices(b):
+    """Parts of larger tensors that do not start on 16 bytes, all at once, give what their copies give; in a captured
+    call the values at the time of the replay count."""
+    seqs, m, nkv, nq, d, per = 3, 3, 2, 4, 64, 5
+    k, v, q = (_randn(i, seqs, m, h, d) for i, h in ((1, nkv), (2, nkv), (3, nq)))
+    pages = torch.randperm(4 * per).to(torch.int32).view(4, per).cuda()
+    pos, count, lens = _int([99, 5, 70, 33]), _int([99, 3, 2, 1]), _int([99, 8, 72, 34])
+    mask = torch.tensor([[0] * m, [1, 2, 5], [1, 3, 7], [1, 1, 4]], dtype=torch.int64, device="cuda")
+    parts = [t[1:] for t in (pos, count, lens, pages, mask)]
+    assert all(t.is_contiguous() and t.data_ptr() % 16 for t in parts)
+
+    def call(cache, pos, count, lens, pages, mask):
+        out = torch.zeros_like(q)
+        cache.append(k, v, pos, pages=pages, n_rows=count)
+        cache.attention(q, lens, pages=pages, n_rows=count, mask=mask, out=out)
+        return [out, *cache.read(80, pages=pages, lens=lens)]
+
+    def new():
+        return b.Kv4Cache(4 * per, 16, nkv, d)
+    got, want = call(new(), *parts), call(new(), *[t.clone() for t in parts])
+    for x, y in zip(got, want):
+        assert y.any() and torch.equal(x, y)
+    cache, graph = new(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = call(cache, *parts)
+    pos[2] -= 20
+    lens[2] -= 20
+    graph.replay()
+    torch.cuda.synchronize()
+    later = call(new(), *[t.clone() for t in parts])
+    assert not torch.equal(later[0], want[0])
+    for x, y in zip(got, later):
+        assert torch.equal(x, y)
