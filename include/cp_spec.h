@@ -425,7 +425,8 @@ cp_spec_status cp_spec_kv4_read(const cp_spec_kv4* shape, const void* d_cache, c
  * weight times a value's scale counts with 11 bits (bfloat16) or 22 (float16,
  * float32), and with a weight of 1 standing for the row's largest never finer
  * than 2^-31 of the largest value scale that the row sees in any channel of the
- * head: channels or positions far smaller than that lose bits.
+ * head (of 2^-80 where all are smaller): channels or positions far smaller than
+ * that lose bits.
  * Results do not depend on timing or on the other sequences' contents, but
  * max_pages and the numbers of sequences, heads and rows choose how a long
  * sequence is split, which moves them within rounding.

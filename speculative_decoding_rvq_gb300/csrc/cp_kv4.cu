@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ K
 // down to 2^-20 of S, below that an error of at most 2^-31 of S; fp16 and float32
 // outputs take the rest as a second term (PT = 2: 22 bits down to 2^-9 of S, the
 // same 2^-31 below), since one term would add about as much error
-// as fp16's own rounding.  The sum of p is float32.  Float32 outputs are added
+// as fp16's own rounding.  S counts as 2^-80 at least.  The sum of p is float32.  Float32 outputs are added
 // up outside the tensor core, whose accumulation truncates (QT = 2).
 //
 // The reference m is only moved when a score exceeds it by 8 (p <= 256), so
@@ -423,7 +423,10 @@ __device__ __forceinline__ void kv4_write(const Kv4Attn& P, int b, int h, int rr
 template <int NG, int NT, int QT, int PT>
 __global__ void __launch_bounds__(32 * kKvMaxWarps, kv4_ctas(NG, NT)) kv4_attention_kernel(const __grid_constant__ Kv4Attn P) {
   constexpr int D = 32 * NG, TB = 18 * D, CH = TB / 16, C = 8 * NT, QS = 2 * D + 64, RS = D + 8;
-  constexpr int E0 = 27;                   // biased exponent that the scales of the values start from (2^-100)
+  // Biased exponent that the scales of the values start from: smaller ones count
+  // as 2^-80.  Sums of weights carry 2^(133 - E0) = 2^86 then, and stay finite for
+  // 2^31 positions of 2^8 each.
+  constexpr int E0 = 47;
   constexpr bool QREG = NG * NT * QT <= 4;  // q operands kept in registers
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ float s_fac[C];

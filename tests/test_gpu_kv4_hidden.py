@@ -90,3 +90,26 @@ def test_a_value_weighed_with_zero_still_counts(b, at, dtype):
             assert torch.isnan(o[0, i, :, 32:]).all(), i
         else:
             assert torch.isfinite(o[0, i]).all(), i
+
+
+@pytest.mark.parametrize("value", [0.0, 2.0 ** -110])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_sums_of_many_tiny_values(b, dtype, value):
+    """2^19 positions of 160 sequences (one run of pages: nothing is split), whose values are zero or far below the
+    smallest scale that the weights are brought to, and whose scores lie just below the step at which the reference
+    moves: the sum of the weights stays finite."""
+    n, seqs = 1 << 19, 160
+    cache = b.Kv4Cache(n // 64, 64, 1, 64)
+    pages = torch.arange(n // 64, dtype=torch.int32, device="cuda").expand(seqs, -1).contiguous()
+    k = torch.full((1, n, 1, 64), 6.0, dtype=DTYPES[dtype], device="cuda")
+    k[:, :256] = 0.0  # the first pairs of tiles of the eight warps
+    cache.append(k, torch.full_like(k, value), _int([0]), pages=pages[:1])
+    q = torch.full((seqs, 1, 1, 64), 5.4 / (6 * 64), dtype=DTYPES[dtype], device="cuda")
+    o, lse = cache.attention(q, _int([n] * seqs), pages=pages, scale=1.0, want_lse=True)
+    s = 6.0 * float(q.double().sum()) / seqs  # 5.4 = 7.8 in powers of two
+    want = s + torch.log(torch.tensor(n - 256 + 256 * 2.718281828459045 ** -s, dtype=torch.float64)).item()
+    # a lane adds 2^13 weights in float32 (2^-24 of the sum each, in the worst case all to one side)
+    assert torch.isfinite(lse).all() and float((lse.double() - want).abs().max()) <= 2.0 ** -11 + 2.0 ** -18
+    # scales count as 2^-80 at least, so a product of 2^86 times the scale may be off by half of fp16's smallest step, 2^-25,
+    # times a code of at most 6, over a weight of 2^7.79: 2^-116.2; the output's rounding 2^-118
+    assert float((o.double() - value).abs().max()) <= (2.0 ** -115 if value else 0.0)
