@@ -335,6 +335,9 @@ cp_spec_status cp_spec_accept_batch(int32_t R, int32_t N, int32_t V, int32_t top
  * E2M1 number nearest to x / s, ties to the even code, saturating at 6.  A
  * group that holds an infinity or a NaN reads back as NaN; one whose scale
  * rounds to zero reads back as zeros.
+ * Any finite x is held like that; the product and the attention are made for
+ * weights, keys and values of at most 2^100 in magnitude (beyond, a group's sum
+ * may overflow where the result would not, and small weights of a softmax drop out).
  *
  * Element types (dtype, out_dtype): 0 float32, 1 bfloat16, 2 float16.  Row
  * strides count elements; a row itself is dense. */
@@ -362,7 +365,8 @@ cp_spec_status cp_spec_w4_unpack(int32_t n, int32_t k, int32_t group, int32_t dt
  * d_x [rows][k] of dtype with row stride x_stride >= k, d_y (out) [rows][n] of
  * out_dtype (dtype, or 0) with row stride y_stride >= n; nothing between the
  * rows of d_y is written.  Sums in float32; float32 inputs count with 22 bits,
- * the 16-bit types exactly (down to 2^-29 of the largest of 128 neighbours).
+ * the 16-bit types exactly, neither finer than 2^-39 of the largest of the 128
+ * neighbours (columns 128 j ..) that an input has.
  * The order of the sums depends on the shape only: a row's result does not
  * depend on the values of the rows beside it. */
 cp_spec_status cp_spec_w4_gemv(int32_t rows, int32_t n, int32_t k, int32_t group, int32_t dtype, int32_t out_dtype,
