@@ -168,8 +168,8 @@ typedef struct {
   int64_t drafted_by_offset[9];
   int64_t accepted_by_offset[9];
   int64_t weight_bytes, kv_bytes, heads_applied;
-  /* Pass kernels executed on the device (5 per layer + lm_heads, top-k and
-   * accept, per pass; counted by the accept kernel). */
+  /* Pass kernels executed on the device (5 per layer, 6 with a 4-bit KV cache,
+   * + lm_heads, top-k and accept, per pass; counted by the accept kernel). */
   int64_t kernel_launches;
   int64_t reserved[7];
 } cp_spec_stats;
@@ -246,7 +246,10 @@ cp_spec_status cp_spec_init_tree(const cp_spec_model* model, const cp_spec_weigh
  * and layer) of 0.14 of its bytes, at the price of the keys' and values' own
  * rounding; greedy codes of different windows may then differ where a value
  * lies as close to a rounding border as float32 sums differ.  Made for few
- * rows per pass: every block of 8 rows reads the weights again.
+ * rows per pass: every block of 8 rows reads the weights again, so packed and
+ * bfloat16 weights are about even at 8 streams and bfloat16 ones 3 to 4.5 times
+ * faster at 64.  The 4-bit cache saves memory, not time (N = 4, one stream: 186
+ * against 159 us per pass).
  * Limits beside cp_spec_init's: head_dim a multiple of 32, vocab of 16; kv_bits
  * 4 needs head_dim 64, 128 or 256 and chain rounds. */
 typedef struct {
@@ -272,7 +275,8 @@ cp_spec_status cp_spec_set_stream_sampling(cp_spec_ctx* ctx, int32_t n, const in
  * int32 first codes; d_codes (out): [n_frames][n_streams][G] int32, with
  * d_codes[f][b][0] = c_0.  Frame f uses Philox frame index first_frame + f.
  * One launch of the context's call graph on `stream` (a setup kernel, then
- * a device-controlled loop of decoder passes, 5 L + 3 kernels each, until
+ * a device-controlled loop of decoder passes, 5 L + 3 kernels each (6 L + 3
+ * with a 4-bit KV cache), until
  * every stream has finished its frames; the graph is built and instantiated
  * on the first call, in host memory); streams advance through their frames
  * independently.  Asynchronous. */

@@ -4,9 +4,9 @@
 // A value is s * c with c one of the sixteen E2M1 numbers (+-0, 0.5, 1, 1.5,
 // 2, 3, 4, 6) and s the bfloat16 scale of its group.  s = bf16(max |x| * r), r
 // the float32 number nearest to 1/6, the product rounded to float32 and then to
-// bfloat16, both to nearest even (for bfloat16 and fp16 inputs the same as
-// max |x| / 6; for float32 inputs 1.5 groups in a million get the neighbouring
-// scale); c is the E2M1 number nearest to x / s, ties to the even code.  The float32 quotient decides like the exact one: a tie
+// bfloat16, both to nearest even (the same as bf16(max |x| / 6) for bfloat16 and
+// fp16 inputs and for all but 21 of the 2^23 significands of float32, where it is
+// the next bfloat16 number); c is the E2M1 number nearest to x / s, ties to the even code.  The float32 quotient decides like the exact one: a tie
 // point is s times a number of at most three bits, hence a float32 number,
 // and for any other x the quotient differs from the tie point by more than
 // half an ulp.  A group that holds an infinity or a NaN gets a NaN scale (all

@@ -59,9 +59,10 @@ __device__ __forceinline__ unsigned char* kv4_tile(const Kv4Map& M, int page, in
 // value codes; where only one of its tokens is written the other's nibbles
 // are left by an atomic exclusive-or of the nibbles that change (another
 // sequence, or another call, may be writing them).  Bound by the bytes of the
-// rows; what it took was 16-byte loads and quotients of three instructions
-// (4 x 8192 tokens of 8 x 128 channels, bfloat16: 113 us with 4 channels a
-// thread, 8-byte loads and packed nibbles spread for the values).
+// rows at a few of them, by the quotients at many (16-byte loads and quotients
+// of three instructions; 4 x 8192 tokens of 8 x 128 channels: bfloat16 58.6 us,
+// 2.9 TB/s, float32 with twice the bytes 60.7 us, 5.0 TB/s; 113 us for bfloat16
+// with 4 channels a thread, 8-byte loads and packed nibbles spread for the values).
 struct Kv4Rows {
   Kv4Map map;
   const void* k;
@@ -326,20 +327,27 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ K
 // down to 2^-20 of S, below that an error of at most 2^-31 of S; fp16 and float32
 // outputs take the rest as a second term (PT = 2: 22 bits down to 2^-9 of S, the
 // same 2^-31 below), since one term would add about as much error
-// as fp16's own rounding.  S counts as 2^-80 at least.  The sum of p is float32.  Float32 outputs are added
-// up outside the tensor core, whose accumulation truncates (QT = 2).
+// as fp16's own rounding.  S counts as 2^-80 at least.  For bfloat16 outputs one
+// term is an eighth of their own rounding (0.0016 off the 64-bit result with one
+// or two terms), and a second one costs: 32 windows of 4 rows 73.4 against 63.5 us
+// a call, one row over 32768 tokens 22.7 against 21.4.  The sum of p is float32.
+// Float32 outputs are added up outside the tensor core, whose accumulation
+// truncates (QT = 2); the 16-bit types inside it, up to 3e-8 for every 128 tokens
+// of an unsplit sequence (8192 steps, 2^20 tokens: 2.5e-4, half of fp16's rounding).
 //
 // The reference m is only moved when a score exceeds it by 8 (p <= 256), so
 // most tiles need no reduction across lanes.
 //
-// Bound: the integer pipe.  Per 32 tokens of a head of 128 channels a warp
-// converts 256 pairs of codes (96 byte extractions, 128 conversions: about
-// 100 of the 192 clocks that HBM takes for the 4608 bytes), applies 64 scales
-// and packs and transposes the weights; the tensor pipe is 22 % busy.
-// Measured: 32 windows of 4 rows, 16 / 8 heads x 128, 4193 to 8192 tokens,
-// bfloat16: 62.2 us, 4.0 TB/s (60 us with every page in L2); one row over 32768
-// tokens, 32 / 8 heads: 18.9 us; 64 windows over 16 tokens: 7.4 us, a chain of
-// latencies.
+// Bound: instructions where an SM holds two CTAs, and uneven shares of the work.
+// Per 32 tokens of a head of 128 channels a warp converts 256 pairs of codes (96
+// byte extractions, 128 conversions: about 100 of the 192 clocks that HBM takes
+// for the 4608 bytes), applies 64 scales and packs and transposes the weights.
+// 304 CTAs of one length, two on each of the 152 SMs, read 5.0 TB/s (74 % of the
+// measured bandwidth); 152, one on each, 3.8, whether from HBM or from L2.
+// Measured: 32 windows of 4 rows, 16 / 8 heads x 128, 5185 to 8192 tokens,
+// bfloat16: 61.9 us, 4.0 TB/s: 256 CTAs leave 48 SMs with one, and the busiest SM
+// works 1.17 times the mean; one row over 32768 tokens, 32 / 8 heads: 19.1 us; 64
+// windows over 16 tokens: 7.6 us, a chain of latencies.
 struct Kv4Attn {
   Kv4Map map;
   const void* q;

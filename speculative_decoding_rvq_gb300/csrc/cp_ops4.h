@@ -1,5 +1,5 @@
 // cp_ops4.h -- launchers of the 4-bit operators (cp_w4.cu, cp_kv4.cu), called
-// by the C ABI in cp_ops4.cu after its checks of arguments.
+// by the C ABI in cp_spec.cu after its checks of arguments.
 #pragma once
 #include <cuda_runtime.h>
 #include <stddef.h>

@@ -24,7 +24,9 @@ namespace cpk {
 // ---------------------------------------------------------- pack, unpack
 // One warp per tile: each lane takes four consecutive columns of each of the
 // 16 rows, and the lanes of a group share its largest magnitude.  Runs once
-// per matrix.
+// per matrix, and is bound by the chain of a row's load, shuffles and quotients
+// (65536 x 4096 bfloat16 in groups of 32: 378 us, floor 101; the way back, with
+// two-byte stores, 151 us).
 __global__ void __launch_bounds__(256) w4_pack_kernel(const void* w, int dtype, long long stride, bool vec, int N, int K,
                                                       int KB, int group, unsigned char* out) {
   const long long tile = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -95,15 +97,19 @@ __global__ void __launch_bounds__(256) w4_unpack_kernel(const unsigned char* pac
 // group's scale and the block's power of two are applied in float32, so the
 // tensor core's truncating accumulation never runs over more than a group.
 //
-// Bound: the bytes of w for a large matrix and a row (1 x 65536 x 4096, groups
-// of 128: 28.7 us, 4.8 TB/s, 71 % of the measured bandwidth; 137 instructions
-// per tile, 56 of them to convert its codes).  Deep rings rather than wide
-// tiles keep them streaming; the A operand is built in registers straight from
-// the codes, so nothing but x and the copies goes through shared memory.  Small
+// Bound: for a large matrix and a row the latency of conversions and MMAs, and
+// how the tiles divide over the SMs: 1 x 65536 x 4096 in groups of 128 takes 28.7
+// us, 4.8 TB/s, 71 % of the measured bandwidth (137 instructions per tile, 56 of
+// them to convert its codes; issue slots 61 %, ALU 47 % busy).  Its 512 groups of
+// tiles go to 256 CTAs, so the busiest SM works 1.12 times the mean; 77824 rows,
+// four groups on each SM, run at 5.5 TB/s, 116736 at 5.8.  Deep rings rather than
+// wide tiles keep the bytes streaming; the A operand is built in registers straight
+// from the codes, so nothing but x and the copies goes through shared memory.  Small
 // products are a chain of latencies (1 x 4096 x 1024: 3.7 us), those with many
 // columns are bound by the conversion of x, which every CTA does for its share
 // of K (8 x 2048 x 6144: 6.7 us, 15 us without the cluster's split), and by
-// instruction latency (64 x 12288 x 2048: 24.9 us).
+// instruction latency and shares (64 x 12288 x 2048: 24.9 us, the weights
+// converted again for every 16 rows; 9728 rows 18.8 us).
 struct W4Gemv {
   const void* x;
   const unsigned char* w;

@@ -1,6 +1,6 @@
 // cp_w4.cuh -- parts that the products with 4-bit weights share: the public
 // operator (cp_w4.cu) and the decoder pass of a context over packed weights
-// (cp_w4_pass.cuh).  The packed layout is described in cp_w4.cu.
+// (cp_w4_pass.cu).  The packed layout is described in cp_w4.cu.
 #pragma once
 #include "cp_fp4.cuh"
 
