@@ -483,7 +483,7 @@ def w4_unpack(w: W4Matrix, dtype=None):
 
 def w4_gemv(x, w: W4Matrix, out=None, out_dtype=None):
     """x [rows, k] times the packed matrix: [rows, n] of x's type (or float32; asynchronous)."""
-    lib = _lib if _torch is not None else _fast()
+    lib = _lib if _torch is not None and _lib is not None else _fast()
     n, k, dt, dev, shape, st = w.n, w.k, x.dtype, x.get_device(), x.shape, x.stride()
     if len(shape) != 2 or shape[1] != k or (st[1] != 1 and k > 1):
         _refuse(f"x: [rows, {k}] with dense rows wanted")

@@ -84,3 +84,12 @@ def test_contexts_refuse_short_matrices(monkeypatch):
             return (n + 15) // 16 * ((k + 127) // 128) * (1024 + 32 * (128 // group))
     monkeypatch.setattr(b, "load", lambda: Sizes())
     assert "bytes" in _refused(lambda: b.CpSpec(SPEC, _packed(), 4, 50, 0.9, 1))
+
+
+def test_a_missing_library_says_so_every_time(monkeypatch):
+    """The second call too (PyTorch is imported by then)."""
+    monkeypatch.setattr(b, "_lib", None)
+    monkeypatch.setattr(b, "LIB_PATH", "/nowhere/libcpspec.so")
+    for _ in range(2):
+        with pytest.raises(RuntimeError, match="not built"):
+            b.w4_gemv(torch.zeros(2, 128), _matrix(16, 128, 32))
