@@ -29,7 +29,7 @@ EXPORTS = ("cp_spec_workspace_bytes", "cp_spec_init", "cp_spec_set_stream_sampli
            "cp_spec_workspace_bytes_tree", "cp_spec_init_tree", "cp_spec_w4_bytes", "cp_spec_w4_pack",
            "cp_spec_w4_unpack", "cp_spec_w4_gemv", "cp_spec_kv4_bytes", "cp_spec_kv4_append", "cp_spec_kv4_read",
            "cp_spec_kv4_attention", "cp_spec_kv4_attention_bytes", "cp_spec_workspace_bytes_w4", "cp_spec_init_w4")
-MAX_W4_K, MAX_KV4_ROWS = 32768, 64
+MAX_W4_N, MAX_W4_K, MAX_KV4_ROWS = 1 << 30, 32768, 64
 
 
 class CpSpecError(RuntimeError):
@@ -460,6 +460,8 @@ class W4Matrix:
 def w4_pack(w, group: int = 32) -> W4Matrix:
     """Quantise w [n, k] (float32, bfloat16 or float16, rows dense) to 4 bits with a scale per `group` columns."""
     lib = _fast()
+    if w.dim() == 2 and w.shape[0] > MAX_W4_N:
+        _refuse(f"w: {w.shape[0]} rows, at most {MAX_W4_N} wanted")
     if w.dim() != 2 or (w.shape[1] > 1 and w.stride(1) != 1):
         _refuse("w: a matrix with dense rows wanted")
     n, k = w.shape
@@ -488,6 +490,8 @@ def w4_gemv(x, w: W4Matrix, out=None, out_dtype=None):
     if len(shape) != 2 or shape[1] != k or (st[1] != 1 and k > 1):
         _refuse(f"x: [rows, {k}] with dense rows wanted")
     rows = shape[0]
+    if rows > 65535:
+        _refuse(f"x: {rows} rows, at most 65535 wanted")
     code, stream = _elem_type(dt), _stream_on(dev)
     if w.data.get_device() != dev:
         _refuse("x and the packed matrix on one device wanted")
@@ -517,6 +521,8 @@ class Kv4Cache:
 
     def __init__(self, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, device="cuda"):
         lib = _fast()
+        if max(n_pages, page_size, n_kv_heads, head_dim) > 0x7FFFFFFF:
+            _refuse("sizes of 31 bits wanted")
         self.shape = Kv4(n_pages, page_size, n_kv_heads, head_dim)
         self._shape = C.addressof(self.shape)
         nbytes = lib.cp_spec_kv4_bytes(self._shape)

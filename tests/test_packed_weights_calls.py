@@ -86,6 +86,17 @@ def test_contexts_refuse_short_matrices(monkeypatch):
     assert "bytes" in _refused(lambda: b.CpSpec(SPEC, _packed(), 4, 50, 0.9, 1))
 
 
+def test_sizes_beyond_32_bits_are_refused(no_library):
+    """The library takes 32-bit sizes: a larger one must not reach it as its low half."""
+    many = (1 << 32) + 16
+    assert "rows" in _refused(lambda: b.w4_pack(torch.zeros(1, 1).expand(many, 1)))
+    assert "rows" in _refused(lambda: b.w4_gemv(torch.zeros(1, 1).expand(many, 1), _matrix(16, 1, 32)))
+    for at in range(3):
+        sizes = [8, 16, 2, 64]
+        sizes[at] += 1 << 32
+        _refused(lambda: b.Kv4Cache(*sizes, device="cpu"))
+
+
 def test_a_missing_library_says_so_every_time(monkeypatch):
     """The second call too (PyTorch is imported by then)."""
     monkeypatch.setattr(b, "_lib", None)
