@@ -577,7 +577,9 @@ cp_spec_status cp_spec_kv16_append(const cp_spec_kv16* shape, void* d_cache, int
  * or NaN among the values reaches every row that sees it.
  * Scores, sums and the softmax are float32.  A weight enters the product with the
  * values as a sum of two numbers of the cache's type, or, where many rows of a
- * sequence share the tiles of the tensor cores, as one.  Results do not depend on
+ * sequence share the tiles of the tensor cores, as one; an fp16 weight far below
+ * its row's largest is off by up to 2^-40 of that largest besides, as one number by
+ * 2^-32, or 2^-38 where those around it are as small.  Results do not depend on
  * timing or on the other sequences' contents, but the call's sizes choose the
  * kernel and how a long sequence is split, which moves them within rounding.
  * d_work: cp_spec_kv16_attention_bytes of scratch (NULL where that is 0), used

@@ -32,6 +32,9 @@ struct Kv16Call {
   long long qs, os;
   int n_pages, page_shift, box_shift, nkv, max_pages, n_seqs, n_rows, max_rows, nq, group, window, sinks, splits, mtiles;
   float scale_log2;  // scale * log2(e): weights are powers of two
+  // A row's weights are 2^(score - base), its base `lift` below a score that was its largest (kv16_base); unlift: 2^-lift.
+  // The tiles of cp_kv16_prompt.cu keep a base until a score passes it by `grow`.
+  float lift, unlift, grow;
   int qvec, ovec;    // rows on 16 bytes
 };
 
@@ -225,6 +228,17 @@ __device__ __forceinline__ float kv16_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// The base of a row whose largest score is `top`.  fp16 numbers end at 2^16 and have steps of 2^-24 below 2^-14: weights
+// that reach 2^15 instead of 1 keep 15 binary orders more of a long tail.  Rounded up there, so that no weight passes 2^lift
+// where float32's steps are coarse.
+template <bool BF>
+__device__ __forceinline__ float kv16_base(float top, float lift) { return BF ? top - lift : __fsub_ru(top, lift); }
+
+// The log of a row's sum of exponentials, from its base and its sum of weights.
+__device__ __forceinline__ float kv16_lse(const Kv16Call& P, float base, float sum) {
+  return sum == 0.0f ? -INFINITY : ((base + P.lift) + log2f(sum * P.unlift)) * 0.693147180559945309f;
 }
 
 // Infinities and NaN of a pair of 16-bit numbers replaced by zero; `bad` is set if there were any.

@@ -20,7 +20,8 @@
 // chain of latencies (lengths, pages, tiles, two products, join).
 //
 // Weights enter the product with the values as a sum of two 16-bit numbers (16
-// bits of bfloat16 pairs, 22 of fp16): the second MMA hides behind the copies.
+// bits of bfloat16 pairs; 22 of fp16, whose weights reach 2^15 so that they have
+// steps of 2^-39 of the largest): the second MMA hides behind the copies.
 // Blocks of 64 rows (256 channels only) are bound by the MMAs: one number there,
 // as in the tiles of cp_kv16_prompt.cu (two are half as many MMAs again).  2048
 // rows over 4096 positions, 16 / 4 heads x 256: 766 us, 135 TFLOP/s, about what
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kFewThreads, D == 256 ? 1 : 2) kv16_few_kernel
     for (int e = 0; e < 2; ++e) {
       top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
       top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
-      const float next = fmaxf(m[e], top[e]);
+      const float next = fmaxf(m[e], kv16_base<BF>(top[e], P.lift));
       base[e] = next == -INFINITY ? 0.0f : next;
       fade[e] = kv16_exp2(m[e] - base[e]);
       m[e] = next;
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kFewThreads, D == 256 ? 1 : 2) kv16_few_kernel
 #pragma unroll
         for (int j = 0; j < 8; ++j) dst[j] = (unsigned short)(w[j >> 1] >> (16 * (j & 1)));
       }
-      if (c == 0 && P.lse) P.lse[at] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
+      if (c == 0 && P.lse) P.lse[at] = kv16_lse(P, M, L);
     }
   }
 }
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(128) kv16_join_kernel(const __grid_constant__ 
       put(c, y0, y1);
     }
   }
-  if (sub == 0 && lane == 0 && P.lse) P.lse[at] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
+  if (sub == 0 && lane == 0 && P.lse) P.lse[at] = kv16_lse(P, M, L);
 }
 
 }  // namespace cpk
@@ -587,6 +588,10 @@ cudaError_t launch_kv16_attention(const Kv16Shape& S, const Kv16Attention& A, in
   P.splits = p.splits;
   P.mtiles = p.mtiles;
   const bool bf = S.dtype == 1;
+  const float late = p.wm == 0 ? kPromptLate : 0.0f;
+  P.lift = bf ? 0.0f : 15.0f - late;
+  P.unlift = exp2f(-P.lift);
+  P.grow = P.lift + late;
   switch (S.d) {
     case 64: return bf ? attention_launch<64, true>(P, p, kernels, s) : attention_launch<64, false>(P, p, kernels, s);
     case 128: return bf ? attention_launch<128, true>(P, p, kernels, s) : attention_launch<128, false>(P, p, kernels, s);

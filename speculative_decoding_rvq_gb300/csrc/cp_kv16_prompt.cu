@@ -14,11 +14,19 @@
 // brings tiles in by TMA (boxes of 64 channels x up to 64 tokens of a page)
 // through a ring of stages, a lane for each product issues its MMAs.
 //
-// The maximum of a row is kept as it was until a score exceeds it by 2^8: O is
-// then rescaled in TMEM (each row by its own decision, so that no row's bits
+// The base of a row's weights stays until a score exceeds the row's largest by
+// 2^8: O is then rescaled in TMEM (each row by its own decision, so that no row's bits
 // depend on another's), else the weights simply grow; sums are float32, weights
 // enter the product as one 16-bit number (half a step of the type, as much as the
 // output's own rounding; the sum uses the unrounded ones).
+//
+// fp16 weights have steps of 2^-24 and end at 2^16.  The largest is put at 2^7,
+// which leaves the 2^8 above: a weight 2^-21 of it has all its bits.  A row that has
+// one far above the others (a sink) would lose its tail: where all that it
+// sees of 64 positions weighs less than 2^-8, or the least of those among which its base was found less
+// than 2^-20 of the largest, its base goes 2^6 lower, once (`tall`): all bits down to 2^-27 of the largest, steps of 2^-37.  With
+// that base from the start, and so 2^2 of room above, random scores move it again
+// and again: 671 us instead of 513 for the long prompt below in fp16.
 //
 // What a row does not see cannot reach it: masked scores weigh zero, and in
 // tiles that are not seen whole by every row values that are not finite are
@@ -49,6 +57,7 @@ namespace cpk {
 constexpr int kPTile = 128;
 constexpr int kPThreads = 384;  // two warpgroups of rows; a third: copies (warp 8), MMAs (9, 10), values looked over (11)
 constexpr int kPHeld = 8;       // tiles whose page bits are kept
+constexpr float kPTall = 6.0f;  // binary orders by which a row of fp16 weights far apart lowers its base
 constexpr int kPFirst = 3;      // ring items whose copies start before the CTA's first barrier
 
 __host__ __device__ constexpr int prompt_stages(int d) { return d == 64 ? 4 : 2; }  // of keys, and as many of values (an even number)
@@ -408,7 +417,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, sa = tmem + lanes + w * 128, oa = tmem + lanes + 256 + w * D;
     const float sl = P.scale_log2;
     float m = -INFINITY, l = 0.0f;
-    bool ok = true;
+    bool ok = true, tall = false;
     int t = 0;
     for (; (PAIR ? t : 2 * t + w) < n; ++t) {
       const int k = PAIR ? t : 2 * t + w, t0 = T.tile(k0 + k) * kPTile;
@@ -453,21 +462,33 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
         for (bool again = false;; again = true) {
           prompt_weights<BF>(x, f, m == -INFINITY ? 0.0f : m, sa + 32 * half, high, sum);
           // (a maximum of 2^20 and more: the exact products lie off its rounding by whole powers of two)
-          if (again || !__any_sync(0xffffffffu, high > (m == -INFINITY ? -INFINITY : 8.0f) || (fabsf(m) >= 1048576.0f && m != -INFINITY))) break;
+          const bool raise = !BF && !tall && high < -8.0f && high > -INFINITY && m != -INFINITY;
+          if (again || !__any_sync(0xffffffffu, high > (m == -INFINITY ? -INFINITY : P.grow) || (fabsf(m) >= 1048576.0f && m != -INFINITY) || raise)) break;
           // some row's maximum grows: again, each row by its own decision
           const float sign = f < 0.0f ? -1.0f : 1.0f;
           float top = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 64; ++c) top = fmaxf(top, sign * __uint_as_float(x[c]));
           top *= sign * f;
+          float low = INFINITY;  // the lowest score that the row sees
+          if (!BF) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+              const float y = sign * __uint_as_float(x[c]);
+              low = fminf(low, y == -INFINITY ? INFINITY : y);
+            }
+            low *= sign * f;
+          }
           if (!(fabsf(top) < 1048576.0f) && top != -INFINITY && f != 1.0f) {
             // such scores are rounded like the maximum before the difference
 #pragma unroll
             for (int c = 0; c < 64; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * f);
             f = 1.0f;
           }
-          const bool grow = top > m + 8.0f;
-          const float next = grow ? top : m, fade = grow ? kv16_exp2(m - next) : 1.0f;
+          const bool grow = top - m > P.grow;  // (a difference: m + grow may round past it)
+          if (!BF) tall |= raise || (grow && top - low > 20.0f);
+          const float next = grow ? kv16_base<BF>(top, tall ? P.lift + kPTall : P.lift) : (raise ? __fsub_ru(m, kPTall) : m);
+          const float fade = grow || raise ? kv16_exp2(m - next) : 1.0f;
           l *= fade;
           m = next;
           if (t + half > 0) {
@@ -586,7 +607,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
         if (P.splits > 1)
           reinterpret_cast<float2*>(P.work + (long long)P.splits * P.n_rows * P.nq * D)[(long long)split * P.n_rows * P.nq + at] = make_float2(m, l);
         else if (P.lse)
-          P.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+          P.lse[at] = kv16_lse(P, m, l);
       }
       // whole rows' pieces of 16 bytes from shared memory: neighbouring threads, neighbouring pieces
       asm volatile("bar.sync %0, 128;" ::"r"(2 + w) : "memory");

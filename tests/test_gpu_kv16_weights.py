@@ -1,0 +1,115 @@
+"""The softmax weights of the attention over the 16-bit cache as numbers: tails far below the largest weight, values near
+the type's end, the second term of a weight, and rows that share a warp.
+
+Scores are made of few products that float32 holds exactly, so that the distances below count only what the kernels round:
+a score times scale * log2(e) and its distance from the reference (2^-19 of a weight for scores within 2^5), the power of
+two (2^-21), the weight's 16-bit form, sums and the output."""
+import math
+
+import pytest
+
+import kv16_reference as R
+from gpu_common import require_gpu, torch
+from test_gpu_kv16_attention import Setup
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def b():
+    require_gpu()
+    from speculative_decoding_rvq_gb300 import binding
+    return binding
+
+
+def plain(s, scores, values, rows, window=0, sinks=0):
+    """Outputs [rows, dim] and the weights [rows, n], in 64 bits, of causal rows at the end whose scores are the same in every row."""
+    n = scores.numel()
+    see = R.visible(n, rows, window, sinks).cuda()
+    e = torch.where(see, torch.exp(scores - scores.max()), 0.0)
+    p = e / e.sum(-1, keepdim=True)
+    return p @ values, p
+
+
+def write(s, scores, values):
+    """One KV head's keys (channel 0 the score: the queries are 1 there, 0 elsewhere) and values, in every head."""
+    n = scores.numel()
+    s.q.zero_()
+    s.q[..., 0] = 1
+    k = torch.zeros(n, s.cache.n_kv_heads, s.dim, device="cuda")
+    k[..., 0] = scores.view(-1, 1)
+    v = values.unsqueeze(1).expand(n, s.cache.n_kv_heads, s.dim)
+    p = torch.arange(n, device="cuda")
+    s.cache.append(k.to(s.dtype), v.to(s.dtype).contiguous(), s.table[0, p // s.page].long() * s.page + p % s.page)
+    return k[:, 0, 0].to(s.dtype).double(), v[:, 0].to(s.dtype).double()
+
+
+@pytest.mark.parametrize("spread", [0.0, 0.5])
+@pytest.mark.parametrize("gap", [12, 14, 16, 18, 20])
+@pytest.mark.parametrize("rows,nq,nkv,dim,n", [(1, 8, 2, 128, 32768), (5, 4, 2, 64, 9000), (2, 8, 1, 256, 20000), (60, 2, 1, 256, 9000),
+                                                (40, 8, 2, 64, 20000), (200, 4, 2, 128, 32768), (700, 32, 8, 128, 9000)])
+def test_tails_below_a_sink(b, rows, nq, nkv, dim, n, gap, spread):
+    """A first position of value zero outweighs all others by e^gap: the others are the whole output.
+
+    fp16 weights that lie this far apart are held as 2^13 times themselves at least, with steps of 2^-24: off by 2^-38
+    of the largest, and by 2^-11 relative (half a step of one number).  A sum takes at most 1024 additions of 16 positions one
+    after the other, each cutting 2^-23: 2^-13, in the values' sum and in the weights'."""
+    s = Setup(b, [(n, rows)], nq, nkv, dim, 64, FP)
+    g = torch.Generator(device="cuda").manual_seed(gap)
+    scores = spread * torch.randn(n, generator=g, device="cuda")
+    scores[0] = gap
+    values = 1 + 0.25 * torch.rand(n, dim, generator=g, device="cuda")
+    values[0] = 0
+    scores, values = write(s, scores, values)
+    out, lse = s.call(scale=1.0)
+    o, p = plain(s, scores, values, rows)
+    lost = torch.minimum(p, 2.0 ** -38 * p.amax(-1, keepdim=True)) @ values
+    tol = o * (2.0 ** -11 + 2.0 ** -11 + 2 * 2.0 ** -13 + 2 * 2.0 ** -18) + lost + 2.0 ** -25
+    off = (out.double() - o.unsqueeze(1)).abs() / tol.unsqueeze(1)
+    assert float(off.max()) <= 1, float(((out.double() - o.unsqueeze(1)).abs() / o.unsqueeze(1)).max())
+
+
+@pytest.mark.parametrize("window", [48, 700])
+@pytest.mark.parametrize("gap", [12, 16, 20])
+@pytest.mark.parametrize("rows,nq,nkv,dim", [(3, 4, 2, 128), (40, 8, 2, 64), (200, 4, 2, 128), (700, 32, 8, 128), (90, 2, 1, 256)])
+def test_tails_of_a_window_below_its_sink(b, rows, nq, nkv, dim, gap, window):
+    """The same with a window so short that no row sees a whole tile of it, and a longer one; distances as above."""
+    n = 3000
+    s = Setup(b, [(n, rows)], nq, nkv, dim, 16, FP)
+    g = torch.Generator(device="cuda").manual_seed(gap)
+    scores = 0.2 * torch.randn(n, generator=g, device="cuda")
+    scores[0] = gap
+    values = 1 + 0.25 * torch.rand(n, dim, generator=g, device="cuda")
+    values[0] = 0
+    scores, values = write(s, scores, values)
+    out, lse = s.call(scale=1.0, window=window, sinks=1)
+    o, p = plain(s, scores, values, rows, window, 1)
+    lost = torch.minimum(p, 2.0 ** -38 * p.amax(-1, keepdim=True)) @ values
+    tol = o * (2.0 ** -11 + 2.0 ** -11 + 2 * 2.0 ** -13 + 2 * 2.0 ** -18) + lost + 2.0 ** -25
+    off = (out.double() - o.unsqueeze(1)).abs() / tol.unsqueeze(1)
+    assert float(off.max()) <= 1, float(((out.double() - o.unsqueeze(1)).abs() / o.unsqueeze(1)).max())
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("nq,nkv,dim", [(1, 1, 64), (4, 2, 128), (2, 1, 256)])
+def test_the_second_term_of_a_weight_counts(b, nq, nkv, dim, dtype):
+    """Values that cancel: the output is far below the sum of weight * |value|, and its own rounding says nothing.
+
+    A weight as two numbers is off by 2^-16 of itself in bfloat16 (2^-9 twice, and float32's own) and by less than 2^-20
+    in fp16; as one number by up to 2^-9 and 2^-12, here about a third of that for the 40 positions together."""
+    n = 40
+    s = Setup(b, [(n, 1)], nq, nkv, dim, 16, dtype)
+    for seed in range(4):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        scores, values = write(s, torch.randn(n, generator=g, device="cuda"), torch.randn(n, dim, generator=g, device="cuda"))
+        scores[-1] = 2.0  # (a power of two: no rounding)
+        _, p = plain(s, scores, values, 1)
+        values[-1] = -(p[:, :-1] @ values[:-1]) / p[0, -1]
+        scores, values = write(s, scores, values)
+        out, _ = s.call(scale=1.0)
+        o, p = plain(s, scores, values, 1)
+        A = p @ values.abs()
+        rel = 2.0 ** -16 if dtype is BF else 2.0 ** -20
+        tol = R.HALF_STEP[dtype] * o.abs() + A * (rel + 2 * (2.0 ** -19 + 2.0 ** -21) + n * 2.0 ** -23) + (2.0 ** -25 if dtype is FP else 0)
+        assert ((out.double() - o.unsqueeze(1)).abs() <= tol.unsqueeze(1)).all(), float(((out.double() - o.unsqueeze(1)).abs() / A).max())
