@@ -575,7 +575,8 @@ cp_spec_status cp_spec_kv16_append(const cp_spec_kv16* shape, void* d_cache, int
  * exponentials.  A row that sees nothing gives zeros and -infinity.  What is stored
  * at a position that a row does not see cannot reach it, not by a bit; an infinity
  * or NaN among the values reaches every row that sees it.
- * Scores, sums and the softmax are float32.  A weight enters the product with the
+ * Scores, sums and the softmax are float32; sums of finite values stay finite, and
+ * values down to 2^-100 keep their bits.  A weight enters the product with the
  * values as a sum of two numbers of the cache's type, or, where many rows of a
  * sequence share the tiles of the tensor cores, as one; an fp16 weight far below
  * its row's largest is off by up to 2^-40 of that largest besides, as one number by

@@ -230,7 +230,7 @@ __device__ __forceinline__ float kv16_exp2(float x) {
   return y;
 }
 
-// The base of a row whose largest score is `top`.  fp16 numbers end at 2^16 and have steps of 2^-24 below 2^-14: weights
+// The base of a row whose largest score is `top`.  bfloat16: its sums then end where its values do.  fp16 numbers end at 2^16 and have steps of 2^-24 below 2^-14: weights
 // that reach 2^15 instead of 1 keep 15 binary orders more of a long tail.  Rounded up there, so that no weight passes 2^lift
 // where float32's steps are coarse.
 template <bool BF>

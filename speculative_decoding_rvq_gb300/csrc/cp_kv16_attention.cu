@@ -589,7 +589,11 @@ cudaError_t launch_kv16_attention(const Kv16Shape& S, const Kv16Attention& A, in
   P.mtiles = p.mtiles;
   const bool bf = S.dtype == 1;
   const float late = p.wm == 0 ? kPromptLate : 0.0f;
-  P.lift = bf ? 0.0f : 15.0f - late;
+  // bfloat16 weights are put so low that no sum of weight * value over the positions a row sees passes the largest value
+  // (they, and float32, have the range); fp16's values are far from float32's end, its weights are put high (kv16_base).
+  long long seen = (long long)A.max_pages * S.page_size;
+  if (P.window > 0) seen = std::min<long long>(seen, (long long)P.window + P.sinks + CP_SPEC_MAX_TREE_ROWS);
+  P.lift = bf ? -(late + (float)(64 - __builtin_clzll((unsigned long long)seen))) : 15.0f - late;
   P.unlift = exp2f(-P.lift);
   P.grow = P.lift + late;
   switch (S.d) {

@@ -113,3 +113,24 @@ def test_the_second_term_of_a_weight_counts(b, nq, nkv, dim, dtype):
         rel = 2.0 ** -16 if dtype is BF else 2.0 ** -20
         tol = R.HALF_STEP[dtype] * o.abs() + A * (rel + 2 * (2.0 ** -19 + 2.0 ** -21) + n * 2.0 ** -23) + (2.0 ** -25 if dtype is FP else 0)
         assert ((out.double() - o.unsqueeze(1)).abs() <= tol.unsqueeze(1)).all(), float(((out.double() - o.unsqueeze(1)).abs() / A).max())
+
+
+@pytest.mark.parametrize("size", ["largest", "tiny"])
+@pytest.mark.parametrize("rising", [0.0, 5.4])
+@pytest.mark.parametrize("rows,nq,nkv,dim", [(1, 2, 1, 128), (3, 4, 2, 64), (50, 2, 2, 256), (40, 4, 1, 64), (300, 4, 2, 128), (600, 32, 8, 128)])
+def test_values_average_to_themselves(b, rows, nq, nkv, dim, rising, size):
+    """bfloat16's largest value everywhere: so is the mean, though the sum of n of them is not a float32.  And a tiny one.
+
+    rising: the scores grow by 5.4 (7.8 binary orders) from one tile of 128 positions to the next, so that a running
+    maximum that follows late leaves weights above 1.  The sums are off by (n / 16) 2^-23 and the output by half a step,
+    so the value itself comes back, or its neighbour."""
+    n = 1500
+    s = Setup(b, [(n, rows)], nq, nkv, dim, 64, BF)
+    top = torch.finfo(BF).max if size == "largest" else 2.0 ** -100
+    scores, values = write(s, rising * (torch.arange(n, device="cuda") // 128).float(), torch.full((n, dim), top, device="cuda"))
+    values[:, 1::2] *= -1
+    write(s, scores.float(), values.float())
+    out, lse = s.call(scale=1.0)
+    assert torch.isfinite(out).all()
+    assert ((out.double().abs() / top - 1).abs() <= 2.0 ** -8).all()
+    assert (torch.sign(out[..., 0::2].float()) == 1).all() and (torch.sign(out[..., 1::2].float()) == -1).all()
