@@ -418,8 +418,9 @@ __global__ void __launch_bounds__(128) kv16_join_kernel(const __grid_constant__ 
     if (sub + W * k < P.splits) {
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) {
-        x[2 * j] += w * v[k][j].x;
-        x[2 * j + 1] += w * v[k][j].y;
+        // (a share whose weight is zero in float32 still hands on an infinity)
+        x[2 * j] += w == 0.0f && fabsf(v[k][j].x) == INFINITY ? v[k][j].x : w * v[k][j].x;
+        x[2 * j + 1] += w == 0.0f && fabsf(v[k][j].y) == INFINITY ? v[k][j].y : w * v[k][j].y;
       }
     }
   }

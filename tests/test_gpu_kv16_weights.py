@@ -134,3 +134,24 @@ def test_values_average_to_themselves(b, rows, nq, nkv, dim, rising, size):
     assert torch.isfinite(out).all()
     assert ((out.double().abs() / top - 1).abs() <= 2.0 ** -8).all()
     assert (torch.sign(out[..., 0::2].float()) == 1).all() and (torch.sign(out[..., 1::2].float()) == -1).all()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("rows,nq,nkv,dim", [(1, 2, 1, 128), (2, 8, 2, 64), (60, 2, 1, 128), (1, 1, 1, 256)])
+def test_an_infinity_reaches_from_a_share_that_weighs_nothing(b, rows, nq, nkv, dim, bad):
+    """The first half of a split sequence has weights that are zero in float32: an infinite value there still reaches."""
+    n = 6000
+    s = Setup(b, [(n, rows)], nq, nkv, dim, 64, BF)
+    assert n // 64 > 32
+    scores = torch.zeros(n, device="cuda")
+    scores[: n // 2] = -200.0
+    values = torch.ones(n, dim, device="cuda")
+    values[7, 5] = bad
+    write(s, scores, values)
+    out, _ = s.call(scale=1.0)
+    if bad == bad:
+        assert (out[..., 5] == bad).all()
+    else:
+        assert torch.isnan(out[..., 5]).all()
+    keep = [c for c in range(dim) if c != 5]
+    assert torch.equal(out[..., keep], torch.ones_like(out[..., keep]))
