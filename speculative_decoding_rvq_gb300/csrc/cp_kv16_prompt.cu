@@ -463,8 +463,9 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
           prompt_weights<BF>(x, f, m == -INFINITY ? 0.0f : m, sa + 32 * half, high, sum);
           // (a maximum of 2^20 and more: the exact products lie off its rounding by whole powers of two)
           const bool raise = !BF && !tall && high < -8.0f && high > -INFINITY && m != -INFINITY;
-          if (again || !__any_sync(0xffffffffu, high > (m == -INFINITY ? -INFINITY : P.grow) || (fabsf(m) >= 1048576.0f && m != -INFINITY) || raise)) break;
-          // some row's maximum grows: again, each row by its own decision
+          const bool own = high > (m == -INFINITY ? -INFINITY : P.grow) || (fabsf(m) >= 1048576.0f && m != -INFINITY) || raise;
+          if (again || !__any_sync(0xffffffffu, own)) break;
+          // some row's base moves: again, each row by its own decision (one that would have kept its weights gets the same ones)
           const float sign = f < 0.0f ? -1.0f : 1.0f;
           float top = -INFINITY;
 #pragma unroll
@@ -479,13 +480,13 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
             }
             low *= sign * f;
           }
-          if (!(fabsf(top) < 1048576.0f) && top != -INFINITY && f != 1.0f) {
+          if (own && !(fabsf(top) < 1048576.0f) && top != -INFINITY && f != 1.0f) {
             // such scores are rounded like the maximum before the difference
 #pragma unroll
             for (int c = 0; c < 64; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * f);
             f = 1.0f;
           }
-          const bool grow = top - m > P.grow;  // (a difference: m + grow may round past it)
+          const bool grow = own && top - m > P.grow;  // (a difference: m + grow may round past it)
           if (!BF) tall |= raise || (grow && top - low > 20.0f);
           const float next = grow ? kv16_base<BF>(top, tall ? P.lift + kPTall : P.lift) : (raise ? __fsub_ru(m, kPTall) : m);
           const float fade = grow || raise ? kv16_exp2(m - next) : 1.0f;

@@ -10,7 +10,7 @@ import pytest
 
 import kv16_reference as R
 from gpu_common import require_gpu, torch
-from test_gpu_kv16_attention import Setup
+from test_gpu_kv16_attention import Setup, _bits
 
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float16
@@ -155,3 +155,32 @@ def test_an_infinity_reaches_from_a_share_that_weighs_nothing(b, rows, nq, nkv, 
         assert torch.isnan(out[..., 5]).all()
     keep = [c for c in range(dim) if c != 5]
     assert torch.equal(out[..., keep], torch.ones_like(out[..., keep]))
+
+
+@pytest.mark.parametrize("dim,heads", [(64, 1), (128, 2)])
+def test_a_rows_bits_are_its_own_at_large_scores(b, dim, heads):
+    """Scores around 2^20, where float32 has steps of 1/16 and 1/8: a later row's own largest score moves no bit of an
+    earlier row of the same warp."""
+    n, rows = 320, 64  # three tiles: one share, the first and the third through one product
+    s = Setup(b, [(n, rows)], heads, 1, dim, 16, FP)
+    s.q.zero_()
+    s.q[..., 0], s.q[..., 1], s.q[..., 2] = 1024, 2, 2.0 ** -6
+    k = torch.zeros(n, 1, dim, device="cuda")
+    # score * log2(e): 2^20 - 4 or so in the first tile, about 7 more at the first row's own position, far less elsewhere
+    x = (2.0 ** 20 - 4) / 1.4426950408889634
+    k[:128, 0, 0] = math.floor(x / 1024)
+    k[:128, 0, 1] = (x - 1024 * math.floor(x / 1024)) // 2
+    slot = torch.arange(n, device="cuda")
+    at = s.table[0, slot // 16].long() * 16 + slot % 16
+    outs = []
+    for far in (0.0, 800.0):
+        res = []
+        for step in range(16):  # the first row's own score, in steps of 1/16 of a unit
+            k[256, 0, 0], k[256, 0, 1], k[256, 0, 2] = k[0, 0, 0], k[0, 0, 1] + 2, 4.0 * step
+            k[276, 0, 0] = far
+            s.cache.append(k.to(FP), s.v[0], at)
+            out, lse = s.call(scale=1.0)
+            res.append((out[:20].clone(), lse[:20].clone()))
+        outs.append(res)
+    for (o0, l0), (o1, l1) in zip(*outs):
+        assert torch.equal(_bits(o0), _bits(o1)) and torch.equal(_bits(l0), _bits(l1))
