@@ -265,23 +265,73 @@ __device__ __forceinline__ float2 kv16_unpack(uint32_t w) {
   return BF ? bf16x2_to_f2(w) : __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// The sum of the values that are infinite or NaN, in eight channels (from c0
-// on) and at the positions t0 .. t0 + tile - 1 that a row sees, whatever their
-// weights; added to x.
-template <bool BF, int D>
-__device__ __noinline__ void kv16_add_infinite(const Kv16Call& P, const Kv16Seq& s, const Kv16Row& r, int b, int h, int t0, int tile,
-                                               int c0, float (&x)[8]) {
-  for (int j = t0; j < t0 + tile && j < s.len; ++j) {
-    if (!kv16_sees(P, s, r, j)) continue;
-    const int page = kv16_page(P, b, j);
-    if (page < 0) continue;
-    const int in = j & ((1 << P.page_shift) - 1);
-    const uint32_t* v = reinterpret_cast<const uint32_t*>(P.values + ((((long long)page * P.nkv + h) << P.page_shift) + in) * D + c0);
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = __ldg(v + i), e = BF ? 0x7F80u : 0x7C00u;
-      const float2 f = kv16_unpack<BF>(w);
-      if ((w & e) == e) x[2 * i] += f.x;
-      if ((w & (e << 16)) == (e << 16)) x[2 * i + 1] += f.y;
+// Values that are not finite, of eight neighbouring channels: bit c (channel c) plus infinity, 8 + c minus infinity, 16 + c
+// NaN.  Or'ed over positions they tell what the sum is, whatever the weights.
+template <bool BF>
+__device__ __forceinline__ uint32_t kv16_odd(const uint4& u) {
+  constexpr uint32_t E = BF ? 0x7F80u : 0x7C00u, ONE = BF ? 0x00800080u : 0x04000400u, EE = E | E << 16;
+  // (an exponent of ones carries into the sign's place when one is added to it)
+  if (((((u.x & EE) + ONE) | ((u.y & EE) + ONE) | ((u.z & EE) + ONE) | ((u.w & EE) + ONE)) & 0x80008000u) == 0) return 0;
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t bits = 0;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t x = w[c >> 1] >> (16 * (c & 1)) & 0xFFFFu;
+    if ((x & E) == E) bits |= 1u << (c + ((x & ~E & 0x7FFFu) ? 16 : (x & 0x8000u ? 8 : 0)));
+  }
+  return bits;
+}
+// What they add up to in channel c, or x if there are none.
+__device__ __forceinline__ float kv16_odd_sum(uint32_t bits, int c, float x) {
+  const uint32_t b = bits >> c;
+  if (b & 0x10000u || (b & 0x101u) == 0x101u) return __int_as_float(0x7FC00000);
+  return b & 1u ? INFINITY : (b & 0x100u ? -INFINITY : x);
+}
+
+template <int D>
+__device__ __forceinline__ uint4 kv16_value(const Kv16Call& P, int page, int h, int j, int c0) {
+  const int in = j & ((1 << P.page_shift) - 1);
+  return __ldg(reinterpret_cast<const uint4*>(P.values + ((((long long)page * P.nkv + h) << P.page_shift) + in) * D + c0));
+}
+
+// Values that are not finite (kv16_odd) in eight channels from c0 on, at the positions first, first + step, .. of each of the
+// tiles k0 .. k0 + n - 1 that all rows i0 .. i1 see whole (pages apart).  Shared by the rows: with these tiles looked
+// over by a warp or more, a NaN costs a few passes over the values (2048 rows over 16384 positions, 8 / 2 heads x 128: 0.23 ms
+// without one, 2.0 with one; 79 where each row looked for itself; one row over 65536: 0.06 and 0.15).  shown: all tiles; else those with pages that are not.
+template <bool BF, int D, int TILE>
+__device__ __noinline__ uint32_t kv16_odd_shared(const Kv16Call& P, const Kv16Seq& s, const Kv16Tiles& T, int b, int h, int i0, int i1,
+                                                 int k0, int n, int c0, int first, int step, bool shown) {
+  uint32_t bits = 0;
+  for (int k = k0; k < k0 + n; ++k) {
+    const int t0 = T.tile(k) * TILE;
+    if (!kv16_whole<TILE>(P, s, i0, i1, t0)) continue;
+    if (!shown && kv16_every<TILE>(P, s, b, i0, i1, t0)) continue;
+#pragma unroll 8
+    for (int j = t0 + first; j < t0 + TILE; j += step) {
+      const int page = kv16_page(P, b, j);
+      if (page >= 0) bits |= kv16_odd<BF>(kv16_value<D>(P, page, h, j, c0));
+    }
+    if (bits >> 16 == 0xFFu) break;  // (all NaN)
+  }
+  return bits;
+}
+// The same for one row in the other tiles, of which a block of rows has few (the ends of what its rows see), for G times
+// eight channels.
+template <bool BF, int D, int TILE, int G>
+__device__ __noinline__ void kv16_odd_own(const Kv16Call& P, const Kv16Seq& s, const Kv16Row& r, const Kv16Tiles& T, int b, int h, int i0,
+                                          int i1, int k0, int n, int c0, uint32_t (&bits)[G]) {
+  for (int k = k0; k < k0 + n; ++k) {
+    const int t0 = T.tile(k) * TILE;
+    if (kv16_whole<TILE>(P, s, i0, i1, t0)) continue;
+    for (int j0 = t0; j0 < t0 + TILE && j0 < s.len; j0 += 16) {
+      const int page = kv16_page(P, b, j0);
+      if (page < 0) continue;
+#pragma unroll 4
+      for (int j = j0; j < j0 + 16; ++j) {
+        if (j >= s.len || !kv16_sees(P, s, r, j)) continue;
+#pragma unroll
+        for (int g = 0; g < G; ++g) bits[g] |= kv16_odd<BF>(kv16_value<D>(P, page, h, j, c0 + 8 * g));
+      }
     }
   }
 }

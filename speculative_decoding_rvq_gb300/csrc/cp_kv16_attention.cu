@@ -62,7 +62,8 @@ struct FewShared {
   uint64_t full[6], empty[6];
   float m[4][16], l[4][16];
   uint32_t held[6];  // bit g: the page of positions 16 g .. 16 g + 15 of the stage's tile exists
-  int abort, bad;
+  uint32_t odd[32];  // values that are not finite, by eight channels (kv16_odd), of the tiles that all rows see
+  int abort, bad, shown;
 };
 
 template <bool BF>
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(kFewThreads, D == 256 ? 1 : 2) kv16_few_kernel
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 4);
     }
-    sh.abort = sh.bad = 0;
+    sh.abort = sh.bad = sh.shown = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -311,6 +312,11 @@ __global__ void __launch_bounds__(kFewThreads, D == 256 ? 1 : 2) kv16_few_kernel
     if (lane == 0) mbar_arrive(&sh.empty[st]);
   }
   if (bad) sh.bad = 1;
+  float odd = 0.0f;
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n) odd += fmaf(O[n][0], 0.0f, O[n][1] * 0.0f) + fmaf(O[n][2], 0.0f, O[n][3] * 0.0f);
+  if (odd != 0.0f) sh.shown = 1;
+  if (tid < D / 8) sh.odd[tid] = 0;
   if (!ok && P.status) atomicCAS(P.status, 0, kStatusTimeout);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -330,6 +336,14 @@ __global__ void __launch_bounds__(kFewThreads, D == 256 ? 1 : 2) kv16_few_kernel
     *reinterpret_cast<float2*>(sums + (g + 8) * (D + 4) + n * 8 + 2 * t) = make_float2(O[n][2], O[n][3]);
   }
   asm volatile("bar.sync 1, 128;" ::: "memory");
+  // Values that are not finite: those left out of tiles that some row does not see whole, and all of them where a sum shows one.
+  const bool left = sh.bad != 0, shown = sh.shown != 0;
+  if (left || shown) {
+    const int c = tid % (D / 8);
+    const uint32_t bits = kv16_odd_shared<BF, D, kFewTile>(P, s, T, b, h, i0, i1, k0, k1 - k0, 8 * c, tid / (D / 8), 128 / (D / 8), shown);
+    if (bits) atomicOr(&sh.odd[c], bits);
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+  }
   for (int e = tid; e < ROWS * (D / 8); e += 128) {
     const int row = e / (D / 8), c = e % (D / 8), r = r0 + row;
     if (r >= packed) continue;
@@ -347,21 +361,11 @@ __global__ void __launch_bounds__(kFewThreads, D == 256 ? 1 : 2) kv16_few_kernel
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] += f * from[j];
     }
-    float fine = 0.0f;
+    if (fabsf(L) < INFINITY && (left || shown)) {  // (with a NaN among the scores the row is NaN anyway)
+      uint32_t bits[1] = {sh.odd[c]};
+      kv16_odd_own<BF, D, kFewTile, 1>(P, s, kv16_row(P, s, i), T, b, h, i0, i1, k0, k1 - k0, 8 * c, bits);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) fine = fmaf(x[j], 0.0f, fine);
-    // Values that are not finite: those left out of tiles that some row does not see whole, and all of them where a sum
-    // shows one.  (With a NaN among the scores the row is NaN anyway.)
-    if (fabsf(L) < INFINITY && (sh.bad || fine != 0.0f)) {
-      const Kv16Row vis = kv16_row(P, s, i);
-      float inf[8] = {};
-      for (int k = k0; k < k1; ++k) {
-        const int t0 = T.tile(k) * kFewTile;
-        if (fine != 0.0f || !kv16_every<kFewTile>(P, s, b, i0, i1, t0)) kv16_add_infinite<BF, D>(P, s, vis, b, h, t0, kFewTile, 8 * c, inf);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (inf[j] != 0.0f) x[j] = inf[j];
+      for (int j = 0; j < 8; ++j) x[j] = kv16_odd_sum(bits[0], j, x[j]);
     }
     const long long at = (long long)(s.start + i) * P.nq + hq;
     if (P.splits > 1) {

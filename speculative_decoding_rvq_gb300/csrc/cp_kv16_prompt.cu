@@ -568,7 +568,6 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = 0;
         }
-        if (!write) continue;
         float fine = 0.0f, y[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
@@ -578,18 +577,21 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
         }
         // Values that are not finite: those left out of tiles that some row does not see whole, and all of them
         // where a sum shows one.  (With a NaN among the scores the row is NaN anyway.)
-        if (fabsf(l) < INFINITY && (fine != 0.0f || bad)) {
-          for (int g = 0; g < 4; ++g) {
-            float inf[8] = {};
-            for (int k = 0; k < n; ++k) {
-              const int t0 = T.tile(k0 + k) * kPTile;
-              if (fine != 0.0f || !kv16_every<kPTile>(P, s, b, i0, i1, t0)) kv16_add_infinite<BF, D>(P, s, vis, b, h, t0, kPTile, c + 8 * g, inf);
-            }
+        const bool shown = write && fabsf(l) < INFINITY && fine != 0.0f, any = __any_sync(0xffffffffu, shown);
+        if (any || bad) {
+          // the warp together for the tiles that all rows see, a lane every eighth position of eight channels
+          uint32_t bits = kv16_odd_shared<BF, D, kPTile>(P, s, T, b, h, i0, i1, k0, n, c + 8 * (lane & 3), lane >> 2, 8, any), own[4];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j / 8 == g && inf[j % 8] != 0.0f) y[j] = inf[j % 8];
+          for (int o = 4; o < 32; o <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
+#pragma unroll
+          for (int g = 0; g < 4; ++g) own[g] = __shfl_sync(0xffffffffu, bits, g);
+          if (write && fabsf(l) < INFINITY) {
+            kv16_odd_own<BF, D, kPTile, 4>(P, s, vis, T, b, h, i0, i1, k0, n, c, own);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] = kv16_odd_sum(own[j / 8], j % 8, y[j]);
           }
         }
+        if (!write) continue;
         if (P.splits > 1) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)

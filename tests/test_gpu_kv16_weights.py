@@ -184,3 +184,37 @@ def test_a_rows_bits_are_its_own_at_large_scores(b, dim, heads):
         outs.append(res)
     for (o0, l0), (o1, l1) in zip(*outs):
         assert torch.equal(_bits(o0), _bits(o1)) and torch.equal(_bits(l0), _bits(l1))
+
+
+@pytest.mark.parametrize("where", ["one", "all", "behind"])
+@pytest.mark.parametrize("rows,nq,nkv,dim,n", [(1, 8, 2, 128, 65536), (2048, 8, 2, 128, 16384), (40, 2, 1, 256, 16384)])
+def test_values_that_are_not_finite_cost_a_few_passes(b, rows, nq, nkv, dim, n, where):
+    """A NaN among the values (one, every value infinite, or garbage behind the last position only) slows a call by a
+    bounded factor; 20 is several times what was measured."""
+    s = Setup(b, [(n - 3, rows)], nq, nkv, dim, 64, BF)
+
+    def time():
+        s.call()
+        torch.cuda.synchronize()
+        best = math.inf
+        for _ in range(3):
+            t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            t0.record()
+            s.call()
+            t1.record()
+            torch.cuda.synchronize()
+            best = min(best, t0.elapsed_time(t1))
+        return best
+
+    clean = time()
+    if where == "one":
+        s.cache.values[int(s.table[0, 1]), :, 5] = float("nan")
+    elif where == "all":
+        s.cache.values.fill_(float("inf"))
+    else:
+        s.cache.data[:, int(s.table[0, (n - 1) // 64]), :, 61:] = float("nan")
+    slow = time()
+    out, _ = s.call()
+    assert torch.isnan(out).all() if where == "one" else (out == float("inf")).all() if where == "all" else torch.isfinite(out).all()
+    print(f"rows {rows} dim {dim} n {n} {where}: {clean * 1e3:.0f} -> {slow * 1e3:.0f} us")
+    assert slow <= 20 * clean + 0.1, (clean, slow)
