@@ -568,7 +568,7 @@ cp_spec_status cp_spec_kv16_append(const cp_spec_kv16* shape, void* d_cache, int
  * nodes of a sparse tree: of its sequence's own rows, a row sees base + j for every
  * bit j of its mask (ancestors and itself), and of the positions below base those
  * that window and sinks leave for p = base + (bits set) - 1, the node's depth.
- *   o = softmax(scale q k^T) v,  scale finite,
+ *   o = softmax(scale q k^T) v,  scale of magnitude at most 2^127,
  * d_q, d_o (out) [n_rows][n_q_heads][head_dim] of the cache's type, row strides in
  * elements; query head e reads KV head e / (n_q_heads / n_kv_heads).  d_lse
  * (optional, out) [n_rows][n_q_heads] float32: the log of the sum of the

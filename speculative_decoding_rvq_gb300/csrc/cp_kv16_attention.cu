@@ -495,7 +495,8 @@ cudaError_t kv16_prepare(const Kv16Shape& S, const Kv16Attention& A, Kv16Call* P
   P->window = (long long)A.window >= (long long)A.max_pages * S.page_size ? 0 : A.window;
   P->sinks = A.sinks;
   P->scale_log2 = (float)((double)A.scale * 1.44269504088896340736);
-  if (P->scale_log2 == 0.0f) P->scale_log2 = 1e-30f;  // (masked scores are infinities that the factor multiplies; all weights are 1 with it)
+  // (masked scores are infinities that the factor multiplies; with float32's least number all weights are 1, whatever the products)
+  if (P->scale_log2 == 0.0f) P->scale_log2 = 1.401298464e-45f;
   P->qvec = ((uintptr_t)A.q & 15u) == 0 && A.qs % 8 == 0;
   P->ovec = ((uintptr_t)A.o & 15u) == 0 && A.os % 8 == 0;
   EncodeTiledFn enc = encode_tiled();

@@ -1203,7 +1203,8 @@ cp_spec_status cp_spec_kv16_attention(const cp_spec_kv16* shape, const void* d_c
                                       size_t work_bytes, int32_t* d_status, void* stream) {
   cp_spec_status v = check_kv16_heads(shape, max_pages, n_seqs, n_rows, max_rows, n_q_heads, window, sinks, d_mask != nullptr);
   if (v != CP_SPEC_OK) return v;
-  if (!std::isfinite(scale)) return fail(nullptr, CP_SPEC_E_INVALID, "scale must be finite");
+  if (!std::isfinite((float)(scale * 1.44269504088896340736)))  // (weights are powers of two)
+    return fail(nullptr, CP_SPEC_E_INVALID, "scale must be finite, of magnitude at most 2^127");
   if (bad_ptr(d_cache) || (d_pages && !aligned16(d_pages))) return fail(nullptr, CP_SPEC_E_INVALID, "cache or page table null or misaligned");
   if (!d_pages && (long long)n_seqs * max_pages > shape->n_pages)
     return fail(nullptr, CP_SPEC_E_INVALID, "without a page table n_seqs * max_pages must not exceed n_pages");

@@ -186,6 +186,20 @@ def test_a_rows_bits_are_its_own_at_large_scores(b, dim, heads):
         assert torch.equal(_bits(o0), _bits(o1)) and torch.equal(_bits(l0), _bits(l1))
 
 
+@pytest.mark.parametrize("rows", [2, 150])
+def test_a_scale_of_zero_is_zero_however_large_the_products(b, rows):
+    s = Setup(b, [(400, rows)], 2, 1, 64, 16, BF)
+    s.q.fill_(1e17)
+    s.cache.keys.mul_(1e17)
+    out, _ = s.call(scale=0.0)
+    v = s.v[0].double()
+    for r in range(rows):
+        n = 400 - rows + r + 1
+        mean = v[:n].mean(0)
+        tol = 2.0 ** -8 * mean.abs() + (n * 2.0 ** -24 + 2.0 ** -20) * v[:n].abs().mean(0)
+        assert ((out[r].double() - mean).abs() <= tol).all(), r
+
+
 @pytest.mark.parametrize("where", ["one", "all", "behind"])
 @pytest.mark.parametrize("rows,nq,nkv,dim,n", [(1, 8, 2, 128, 65536), (2048, 8, 2, 128, 16384), (40, 2, 1, 256, 16384)])
 def test_values_that_are_not_finite_cost_a_few_passes(b, rows, nq, nkv, dim, n, where):
