@@ -166,9 +166,9 @@ __global__ void __launch_bounds__(1024, 1) kv_plan_kernel(const __grid_constant_
   }
   __syncthreads();
   const int step = C * blockDim.x, first = rank * blockDim.x + tid;
-  // pages given back: entry e of the list in order of (sequence, page), pushed from its end
-  for (int e = first; e < (int)given; e += step) {
-    const int b = plan_find(sh.G, P.n_seqs, e);
+  // pages given back: entry e of the list in order of (sequence, page), pushed from its end (up to 2^31 - 1 of them: e passes 31 bits)
+  for (long long e = first; e < given; e += step) {
+    const int b = plan_find(sh.G, P.n_seqs, (int)e);
     int* at = P.pages + (long long)b * P.max_pages + sh.need[b] + (e - sh.G[b]);
     const long long to = n_free + given - 1 - e;
     if (to < P.n_pages) P.free[to] = load_l2(at);
@@ -177,8 +177,8 @@ __global__ void __launch_bounds__(1024, 1) kv_plan_kernel(const __grid_constant_
   if (given > 0 && taken > 0) {  // the same in every CTA
     if (C > 1) cg::this_cluster().sync(); else __syncthreads();
   }
-  for (int e = first; e < taken; e += step) {
-    const int b = plan_find(sh.T, P.n_seqs, e);
+  for (long long e = first; e < taken; e += step) {
+    const int b = plan_find(sh.T, P.n_seqs, (int)e);
     P.pages[(long long)b * P.max_pages + sh.had[b] + (e - sh.T[b])] = load_l2(P.free + (full - 1 - e));
   }
   if (!fill) return;
