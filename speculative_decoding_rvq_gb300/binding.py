@@ -843,9 +843,10 @@ class Kv16Cache:
         """Attention of packed rows q [n_rows, heads, head_dim] over the cache (see cp_spec_kv16_attention).
 
         kv_len int32 [n_seqs] counts a sequence's own rows, which are row_start[b] .. row_start[b + 1] - 1 (int32
-        [n_seqs + 1]), at most max_rows of them (n_rows unless given: the tighter, the faster).  window and sinks: each
-        row sees the last `window` positions and the first `sinks` (window 0: all).  mask int64 [n_rows]: trees, the bits
-        of the sequence's rows that a row sees.  status (int32, one element): set to E_DEVICE_TIMEOUT if a kernel gave up.
+        [n_seqs + 1]), at most max_rows of them: give it for batches, where the most rows of a sequence are far fewer than
+        n_rows, which is taken otherwise.  window and sinks: each row sees the last `window` positions and the first `sinks`
+        (window 0: all).  mask int64 [n_rows]: trees of up to 64 rows (max_rows 64 unless given), the bits of the sequence's
+        rows that a row sees.  status (int32, one element): set to E_DEVICE_TIMEOUT if a kernel gave up.
         Returns the output and with want_lse also the log of the sums of exponentials [n_rows, heads]; rows past the last
         sequence are not written."""
         lib, data, d, dt, shape = _lib or _fast(), self.data, self.head_dim, self.dtype, q.shape
@@ -878,7 +879,7 @@ class Kv16Cache:
                 _refuse(f"pages: [{n}, max_pages] wanted")
             per = shape[1]
             table = _index(pages, n * per, "pages", dev, keep)
-        most = m if max_rows is None else max_rows
+        most = (m if mask is None else min(m, MAX_TREE_ROWS)) if max_rows is None else max_rows
         if not (0 <= most <= 0x7FFFFFFF and 0 <= window <= 0x7FFFFFFF and 0 <= sinks <= 0x7FFFFFFF):
             _refuse("max_rows, window and sinks of 31 bits wanted")
         need = lib.cp_spec_kv16_attention_bytes(self._shape, per, n, m, most, nq, window, sinks, 0 if mask is None else 1)
