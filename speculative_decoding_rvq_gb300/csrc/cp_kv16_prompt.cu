@@ -194,7 +194,9 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
   unsigned char* ring = smem + 2 * SB;  // after the queries of both blocks
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = blockIdx.x % P.splits, mt = P.mtiles - 1 - blockIdx.x / P.splits, h = blockIdx.y, b = blockIdx.z;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // Only the kernel that joins the shares may start early: one that takes tensor memory before it waits for this
+  // kernel could sit beside a CTA that then never gets its own.
+  if (P.splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Kv16Seq s = kv16_seq(P, b);
   const int r0 = mt * ROWS, packed = s.m * P.group;
   if (r0 >= packed) return;
