@@ -26,7 +26,7 @@
 // sees of 64 positions weighs less than 2^-8, or the least of those among which its base was found less
 // than 2^-20 of the largest, its base goes 2^6 lower, once (`tall`): all bits down to 2^-27 of the largest, steps of 2^-37.  With
 // that base from the start, and so 2^2 of room above, random scores move it again
-// and again: 671 us instead of 513 for the long prompt below in fp16.
+// and again: 671 us instead of 485 for the long prompt below in fp16.
 //
 // What a row does not see cannot reach it: masked scores weigh zero, and in
 // tiles that are not seen whole by every row values that are not finite are
@@ -419,6 +419,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, sa = tmem + lanes + w * 128, oa = tmem + lanes + 256 + w * D;
     const float sl = P.scale_log2;
     float m = -INFINITY, l = 0.0f;
+    float high_most = -INFINITY, high_least = -INFINITY;  // exponents between which a half's largest leaves the base where it is
     bool ok = true, tall = false;
     int t = 0;
     for (; (PAIR ? t : 2 * t + w) < n; ++t) {
@@ -463,9 +464,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
 #pragma unroll 1
         for (bool again = false;; again = true) {
           prompt_weights<BF>(x, f, m == -INFINITY ? 0.0f : m, sa + 32 * half, high, sum);
-          // (a maximum of 2^20 and more: the exact products lie off its rounding by whole powers of two)
-          const bool raise = !BF && !tall && high < -8.0f && high > -INFINITY && m != -INFINITY;
-          const bool own = high > (m == -INFINITY ? -INFINITY : P.grow) || (fabsf(m) >= 1048576.0f && m != -INFINITY) || raise;
+          const bool raise = !BF && high < high_least && high > -INFINITY, own = high > high_most || raise;
           if (again || !__any_sync(0xffffffffu, own)) break;
           // some row's base moves: again, each row by its own decision (one that would have kept its weights gets the same ones)
           const float sign = f < 0.0f ? -1.0f : 1.0f;
@@ -494,6 +493,9 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
           const float fade = grow || raise ? kv16_exp2(m - next) : 1.0f;
           l *= fade;
           m = next;
+          // (a base of 2^20 and more: the exact products lie off its rounding by whole powers of two, so every half is gone over again)
+          high_most = fabsf(m) < 1048576.0f ? P.grow : -INFINITY;
+          if (!BF) high_least = tall || m == -INFINITY ? -INFINITY : -8.0f;
           if (t + half > 0) {
             // (the scores of this tile came after the products of the tile before)
             if (half == 1) ok = __all_sync(0xffffffffu, kv16_wait(&sh.ohalf[w], (uint32_t)t & 1u, &sh.abort));
