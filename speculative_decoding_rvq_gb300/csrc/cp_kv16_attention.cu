@@ -149,9 +149,9 @@ __global__ void __launch_bounds__(kFewThreads, D == 256 ? 1 : 2) kv16_few_kernel
       __syncwarp();
       issued = k + 1;
     }
-    if (!ok)  // nothing in flight at exit
-      for (int k = max(k0, issued - STAGES); k < issued; ++k) kv16_drain(&sh.full[(k - k0) % STAGES], (uint32_t)((k - k0) / STAGES) & 1u);
     __syncthreads();
+    if (sh.abort)  // nothing in flight at exit: whoever gave up, copies may not have landed
+      for (int k = max(k0, issued - STAGES); k < issued; ++k) kv16_drain(&sh.full[(k - k0) % STAGES], (uint32_t)((k - k0) / STAGES) & 1u);
     return;
   }
 

@@ -34,8 +34,8 @@
 // a tile as it lands, ahead of its use); the rows that do see them get them
 // at the end, from the cache.
 //
-// Every wait is bounded; one that runs out ends all roles, which first wait
-// for their copies and MMAs in flight.
+// Every wait is bounded; one that runs out ends all roles, and the CTA with them
+// once its copies and MMAs in flight are through.
 //
 // Measured: 8192 rows over 16384 positions, window 4096, 32 / 8 heads x 128: 472
 // us, 1167 TFLOP/s (59 % of the burst rate).  A turn of both blocks of rows takes
@@ -71,7 +71,7 @@ struct PromptShared {
   float m[2][128], l[2][128];
   uint32_t held[kPHeld];
   uint32_t tmem;
-  int abort, bad;
+  int abort, bad, keys, values;  // tiles copied
 };
 
 // Shared-memory descriptors: 128-byte swizzle; K-major rows of 128 bytes in
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
         mbar_init(&sh.oend[w], 1);
         mbar_init(&sh.last[w], 1);
       }
-      sh.abort = sh.bad = 0;
+      sh.abort = sh.bad = sh.keys = sh.values = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -317,9 +317,9 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
         }
         if (a.v) ++values; else ++keys;
       }
-      if (!ok) {  // nothing in flight at exit
-        for (int k = max(0, keys - STAGES); k < keys; ++k) kv16_drain(&sh.kfull[k % STAGES], (uint32_t)(k / STAGES) & 1u);
-        for (int k = max(0, values - STAGES); k < values; ++k) kv16_drain(&sh.vfull[k % STAGES], (uint32_t)(k / STAGES) & 1u);
+      if (lane == 0) {
+        sh.keys = keys;
+        sh.values = values;
       }
     } else if (warp <= 10 && n > 0) {
       // ================= MMAs: a warp for each of the two products, one lane of it waits and issues.  (One warp for
@@ -521,6 +521,10 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
       }
       if (!ok) break;
     }
+    if (!ok) {  // loads and stores of TMEM that were under way
+      tmem_wait_ld();
+      tmem_wait_st();
+    }
     if (ok && t > 0) ok = __all_sync(0xffffffffu, kv16_wait(&sh.oend[w], 0, &sh.abort));
     if (!ok && P.status) atomicCAS(P.status, 0, kStatusTimeout);
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -648,6 +652,10 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   }
   __syncthreads();
+  if (warp == 8 && sh.abort) {  // nothing in flight at exit: whoever gave up, copies may not have landed
+    for (int k = max(0, sh.keys - STAGES); k < sh.keys; ++k) kv16_drain(&sh.kfull[k % STAGES], (uint32_t)(k / STAGES) & 1u);
+    for (int k = max(0, sh.values - STAGES); k < sh.values; ++k) kv16_drain(&sh.vfull[k % STAGES], (uint32_t)(k / STAGES) & 1u);
+  }
   if (warp == 9) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
