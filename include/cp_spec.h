@@ -664,6 +664,9 @@ cp_spec_status cp_spec_reset_stats(cp_spec_ctx* ctx, void* stream);
  * 0 restores normal operation.  Nothing traps or spins without a bound.
  * Packed weights have no bounded wait (bit 0) and a 4-bit cache no float slots
  * (bit 1): CP_SPEC_E_UNSUPPORTED there.
+ * ctx NULL: the waits of cp_spec_kv16_attention, in all later calls of the process;
+ * flags 1: the last copy of every CTA is not made, 2: none is, so that the waits
+ * for it run out and the call's d_status says so.
  * Synchronises the device if the context's call graph exists (it is rebuilt
  * on the next call). */
 cp_spec_status cp_spec_test_hooks(cp_spec_ctx* ctx, uint64_t wait_limit_ns, int32_t flags);

@@ -636,6 +636,13 @@ class Kv4Cache:
 
 
 # ------------------------------------------- 16-bit paged KV cache
+def kv16_test_hooks(wait_limit_ns: int = 2_000_000_000, stall: int = 0):
+    """Diagnostics of Kv16Cache.attention, for the whole process (cp_spec_test_hooks without a context).
+
+    stall 1: the last copy of every CTA is not made, 2: none is; the waits for it run out after wait_limit_ns."""
+    _check(_fast().cp_spec_test_hooks(None, int(wait_limit_ns), stall))
+
+
 class PlanRows:
     """What a step of a PagePool gives: kv_len, refused [n_seqs], row_start [n_seqs + 1], pos, slot [n_rows].
 

@@ -12,8 +12,6 @@
 
 namespace cpk {
 
-constexpr uint64_t kKv16WaitNs = 2000000000ull;  // bound of every wait of these kernels
-
 // One attention call.  Rows of a sequence and KV head are packed: packed row
 // r = i * group + g is row i of the sequence with query head h * group + g.
 struct Kv16Call {
@@ -36,6 +34,8 @@ struct Kv16Call {
   // The tiles of cp_kv16_prompt.cu keep a base until a score passes it by `grow`.
   float lift, unlift, grow;
   int qvec, ovec;    // rows on 16 bytes
+  int stall;         // test hook: 1 the last copy of a CTA is not made, 2 none is
+  uint64_t wait_ns;  // bound of every wait
 };
 
 // The part of a call that belongs to one sequence.
@@ -199,7 +199,7 @@ struct Kv16Pages {
 // Wait for a phase of `bar`, bounded, that also ends when another thread of the
 // CTA gave up.  The clock is read only every 256 tries: reading it takes longer
 // than a wait of these kernels.
-__device__ __forceinline__ bool kv16_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool kv16_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
 #pragma unroll 1
   for (int i = 0; i < 256; ++i)
     if (mbar_try_wait(bar, parity)) return true;
@@ -209,17 +209,17 @@ __device__ __forceinline__ bool kv16_wait(uint64_t* bar, uint32_t parity, volati
     for (int i = 0; i < 256; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
-    if (globaltimer_ns() - t0 > kKv16WaitNs) {
+    if (globaltimer_ns() - t0 > limit_ns) {
       *abort = 1;
       return false;
     }
   }
 }
 
-// Wait for copies in flight after a wait that ran out.
+// Wait for copies and MMAs in flight after a wait that ran out: they were issued, so they do arrive.
 __device__ __forceinline__ void kv16_drain(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < kKv16WaitNs) {
+  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < 2000000000ull) {
   }
 }
 

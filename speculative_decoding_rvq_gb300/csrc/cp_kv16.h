@@ -65,6 +65,8 @@ struct Kv16Attention {
   float scale;
   void* work;
   int* status;  // or null
+  int stall;          // test hook: 1 the last copy of a CTA is not made, 2 none is
+  uint64_t wait_ns;   // bound of every device-side wait
 };
 size_t kv16_attention_work(const Kv16Shape& S, const Kv16Attention& A, int sms);
 cudaError_t launch_kv16_attention(const Kv16Shape& S, const Kv16Attention& A, int sms, int* kernels, cudaStream_t s);

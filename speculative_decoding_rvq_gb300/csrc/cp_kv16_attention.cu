@@ -125,12 +125,13 @@ __global__ void __launch_bounds__(kFewThreads, D == 256 ? 1 : 2) kv16_few_kernel
     pages.start(P, b, T, k0, k1 - k0, end, lane);
     bool ok = true;
     int issued = k0;
+    const int copied = P.stall == 0 ? k1 : (P.stall == 1 ? max(k0, k1 - 1) : k0);
 #pragma unroll 1
-    for (int k = k0; k < k1; ++k) {
+    for (int k = k0; k < copied; ++k) {
       const int st = (k - k0) % STAGES, turn = (k - k0) / STAGES;
       const int id = pages.of(P, b, T, k0, k1 - k0, end, k - k0, lane), lane0 = ((k - k0) & (pages.each - 1)) * pages.per;
       const uint32_t held = pages.held(id, k - k0);
-      if (turn > 0) ok = __all_sync(0xffffffffu, kv16_wait(&sh.empty[st], (uint32_t)(turn - 1) & 1u, &sh.abort));
+      if (turn > 0) ok = __all_sync(0xffffffffu, kv16_wait(&sh.empty[st], (uint32_t)(turn - 1) & 1u, &sh.abort, P.wait_ns));
       if (!ok) break;
       if (lane == 0) {
         sh.held[st] = held;
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(kFewThreads, D == 256 ? 1 : 2) kv16_few_kernel
   bool ok = true, bad = false;
   for (int k = k0; k < k1; ++k) {
     const int st = (k - k0) % STAGES;
-    ok = kv16_wait(&sh.full[st], (uint32_t)((k - k0) / STAGES) & 1u, &sh.abort);
+    ok = kv16_wait(&sh.full[st], (uint32_t)((k - k0) / STAGES) & 1u, &sh.abort, P.wait_ns);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     const uint32_t ks = kb + st * SB, vs = ks + SB / 2;
@@ -494,6 +495,8 @@ cudaError_t kv16_prepare(const Kv16Shape& S, const Kv16Attention& A, Kv16Call* P
   // a window that covers the longest sequence is none
   P->window = (long long)A.window >= (long long)A.max_pages * S.page_size ? 0 : A.window;
   P->sinks = A.sinks;
+  P->stall = A.stall;
+  P->wait_ns = A.wait_ns;
   P->scale_log2 = (float)((double)A.scale * 1.44269504088896340736);
   // (masked scores are infinities that the factor multiplies; with float32's least number all weights are 1, whatever the products)
   if (P->scale_log2 == 0.0f) P->scale_log2 = 1.401298464e-45f;

@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
   const int k0 = (int)((long long)T.n * split / P.splits), n = (int)((long long)T.n * (split + 1) / P.splits) - k0;
 
   // copies of ring items
+  const int items = P.stall == 0 ? 2 * n : (P.stall == 1 ? max(0, 2 * n - 1) : 0);
   const int end = P.mask ? s.len : min(s.len, s.base + i1 + 1);
   Kv16Pages<kPTile> pages;
   auto issue = [&](int it) {
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
     }
     __syncwarp();
 #pragma unroll 1
-    for (int it = 0; it < min(kPFirst, 2 * n); ++it) issue(it);
+    for (int it = 0; it < min(kPFirst, items); ++it) issue(it);
   } else if (warp == 9) {  // all of TMEM: S0, S1, O0, O1
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -307,11 +308,11 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
       bool ok = true;
       int keys = 0, values = 0;  // copied
 #pragma unroll 1
-      for (int it = 0; it < 2 * n; ++it) {
+      for (int it = 0; it < items; ++it) {
         const PromptItem a = prompt_item<PAIR>(it, n);
         if (it >= kPFirst) {
           if (a.k >= STAGES)
-            ok = __all_sync(0xffffffffu, kv16_wait(a.v ? &sh.vempty[a.k % STAGES] : &sh.kempty[a.k % STAGES], (uint32_t)(a.k / STAGES - 1) & 1u, &sh.abort));
+            ok = __all_sync(0xffffffffu, kv16_wait(a.v ? &sh.vempty[a.k % STAGES] : &sh.kempty[a.k % STAGES], (uint32_t)(a.k / STAGES - 1) & 1u, &sh.abort, P.wait_ns));
           if (!ok) break;
           issue(it);
         }
@@ -342,17 +343,17 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
         };
         const int k1 = PAIR ? 0 : w;
         bool ok = true;
-        if (k1 < n) ok = kv16_wait(&sh.kfull[k1 % STAGES], 0, &sh.abort);
+        if (k1 < n) ok = kv16_wait(&sh.kfull[k1 % STAGES], 0, &sh.abort, P.wait_ns);
         if (ok && k1 < n) scores(k1);
 #pragma unroll 1
         for (int t = 0; ok; ++t) {
           const int k = PAIR ? t : 2 * t + w, next = PAIR ? t + 1 : k + 2;
           if (k >= n) break;
-          ok = kv16_wait(&sh.clean[k % STAGES], (uint32_t)(k / STAGES) & 1u, &sh.abort);
+          ok = kv16_wait(&sh.clean[k % STAGES], (uint32_t)(k / STAGES) & 1u, &sh.abort, P.wait_ns);
           const uint64_t vv = vdesc + (k % STAGES) * (SB / 16);
 #pragma unroll 1
           for (int half = 0; half < 2 && ok; ++half) {  // O += P V, half the tokens
-            ok = kv16_wait(&sh.pready[w][half], (uint32_t)t & 1u, &sh.abort);
+            ok = kv16_wait(&sh.pready[w][half], (uint32_t)t & 1u, &sh.abort, P.wait_ns);
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
               prompt_mma_ts(to, ts + half * 32 + c * 8, vv + half * (64 * 128 / 16) + c * (2048 / 16), odesc, t + half + c > 0);
             if (half == 0) {
               prompt_commit(&sh.ohalf[w]);
-              if (next < n) ok = kv16_wait(&sh.kfull[next % STAGES], (uint32_t)(next / STAGES) & 1u, &sh.abort);
+              if (next < n) ok = kv16_wait(&sh.kfull[next % STAGES], (uint32_t)(next / STAGES) & 1u, &sh.abort, P.wait_ns);
             }
           }
           if (!ok) break;
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
       // ================= values looked over, tile by tile as they land
       bool ok = true;
       for (int k = 0; k < n && ok; ++k) {
-        ok = kv16_wait(&sh.vfull[k % STAGES], (uint32_t)(k / STAGES) & 1u, &sh.abort);
+        ok = kv16_wait(&sh.vfull[k % STAGES], (uint32_t)(k / STAGES) & 1u, &sh.abort, P.wait_ns);
         if (!ok) break;
         {
           const int t0 = T.tile(k0 + k) * kPTile;
@@ -424,7 +425,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
     int t = 0;
     for (; (PAIR ? t : 2 * t + w) < n; ++t) {
       const int k = PAIR ? t : 2 * t + w, t0 = T.tile(k0 + k) * kPTile;
-      ok = __all_sync(0xffffffffu, kv16_wait(&sh.sfull[w], (uint32_t)t & 1u, &sh.abort));
+      ok = __all_sync(0xffffffffu, kv16_wait(&sh.sfull[w], (uint32_t)t & 1u, &sh.abort, P.wait_ns));
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       uint32_t xs[2][64];
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
           if (!BF) high_least = tall || m == -INFINITY ? -INFINITY : -8.0f;
           if (t + half > 0) {
             // (the scores of this tile came after the products of the tile before)
-            if (half == 1) ok = __all_sync(0xffffffffu, kv16_wait(&sh.ohalf[w], (uint32_t)t & 1u, &sh.abort));
+            if (half == 1) ok = __all_sync(0xffffffffu, kv16_wait(&sh.ohalf[w], (uint32_t)t & 1u, &sh.abort, P.wait_ns));
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll 1
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv16_prompt_kernel(const __grid_
       tmem_wait_ld();
       tmem_wait_st();
     }
-    if (ok && t > 0) ok = __all_sync(0xffffffffu, kv16_wait(&sh.oend[w], 0, &sh.abort));
+    if (ok && t > 0) ok = __all_sync(0xffffffffu, kv16_wait(&sh.oend[w], 0, &sh.abort, P.wait_ns));
     if (!ok && P.status) atomicCAS(P.status, 0, kStatusTimeout);
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const bool have = t > 0;  // O holds something

@@ -64,6 +64,8 @@ namespace {
 
 thread_local char g_err[512];  // message of the thread's last refused call without a context
 std::atomic<long long> g_free_launches{0};
+std::atomic<uint64_t> g_kv16_wait_ns{2000000000ull};  // cp_spec_test_hooks without a context
+std::atomic<int> g_kv16_stall{0};
 
 cp_spec_status fail(cp_spec_ctx* c, cp_spec_status s, const char* fmt, ...) {
   char buf[512];
@@ -1225,6 +1227,8 @@ cp_spec_status cp_spec_kv16_attention(const cp_spec_kv16* shape, const void* d_c
   A.max_pages = max_pages; A.n_seqs = n_seqs; A.n_rows = n_rows; A.max_rows = std::min(max_rows, n_rows); A.nq = n_q_heads;
   A.window = window; A.sinks = sinks; A.scale = scale;
   A.work = d_work; A.status = d_status;
+  A.stall = g_kv16_stall.load();
+  A.wait_ns = g_kv16_wait_ns.load();
   const size_t need = cpk_host::kv16_attention_work(kv16_shape(shape), A, sms);
   if (need > (d_work ? work_bytes : 0))
     return fail(nullptr, CP_SPEC_E_WORKSPACE, "needs %zu bytes of workspace (cp_spec_kv16_attention_bytes)", need);
@@ -1352,9 +1356,14 @@ cp_spec_status cp_spec_reset_stats(cp_spec_ctx* c, void* stream) {
 }
 
 cp_spec_status cp_spec_test_hooks(cp_spec_ctx* c, uint64_t wait_limit_ns, int32_t flags) {
-  if (!c) return fail(nullptr, CP_SPEC_E_INVALID, "null context");
   if (wait_limit_ns < 10000ull || wait_limit_ns > 60ull * 1000000000ull)
     return fail(c, CP_SPEC_E_INVALID, "wait_limit_ns must be in [1e4, 6e10]");
+  if (!c) {  // the attention over the 16-bit cache
+    if (flags < 0 || flags > 2) return fail(nullptr, CP_SPEC_E_INVALID, "flags must be in [0, 2] without a context");
+    g_kv16_wait_ns.store(wait_limit_ns);
+    g_kv16_stall.store(flags);
+    return CP_SPEC_OK;
+  }
   if (flags < 0 || flags > 3) return fail(c, CP_SPEC_E_INVALID, "flags must be in [0, 3]");
   if ((c->base.w4 && (flags & 1)) || (c->base.kv4 && (flags & 2)))
     return fail(c, CP_SPEC_E_UNSUPPORTED, "packed weights have no bounded wait to stall, a 4-bit cache no float slots to poison");

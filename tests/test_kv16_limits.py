@@ -27,3 +27,10 @@ def test_scales_past_the_range_of_powers_of_two(lib):
         assert attend(scale) == b.E_INVALID, scale
     for scale in (0.0, -0.0, 1e-45, 2.0 ** 127, -(2.0 ** 127)):  # (no rows: nothing is launched)
         assert attend(scale, rows=0) == b.OK, scale
+
+
+def test_hooks_without_a_context(lib):
+    from speculative_decoding_rvq_gb300 import binding as b
+    for ns, flags in ((100, 0), (10 ** 11, 0), (2_000_000_000, 3), (2_000_000_000, -1)):
+        assert lib.cp_spec_test_hooks(None, ns, flags) == b.E_INVALID
+    assert lib.cp_spec_test_hooks(None, 2_000_000_000, 0) == b.OK
