@@ -503,9 +503,11 @@ cp_spec_status cp_spec_kv_plan(int32_t n_seqs, int32_t max_pages, int32_t page_s
 
 /* A rotary embedding: pair i (channels i and i + rot_dim / 2 of a head, the
  * rotate-half pairing of cp_spec_model) turns by the position on its axis times
- * theta^(-2 i / rot_dim); channels from rot_dim on stay.  Filled by
+ * theta^(-2 i / rot_dim), i counted over all axes; channels from rot_dim on stay.  Filled by
  * cp_spec_rope_init, a host function without device work; the struct is read
- * during the calls that take it. */
+ * during the calls that take it.  Another rule (frequencies that begin anew at each
+ * axis, as image encoders have, or scaled ones) is written into turns and axis
+ * after that: any turns, and axis below n_axes. */
 typedef struct {
   int32_t rot_dim, n_axes;
   uint8_t axis[128];   /* axis of each pair                                      */

@@ -726,7 +726,8 @@ def _row_heads(t, dim, what: str, dev: int) -> int:
 class Rope:
     """A rotary embedding over one or several position axes (see cp_spec_rope_init).
 
-    sections: pairs of each axis (None: one axis); interleaved: the axes take turns pair by pair."""
+    sections: pairs of each axis (None: one axis); interleaved: the axes take turns pair by pair.  Pair i has the frequency
+    theta^(-2 i / rot_dim) whatever its axis; other ones are set in struct.turns (turns a position, times 2^64)."""
 
     def __init__(self, rot_dim: int, theta: float, sections=None, interleaved: bool = False):
         lib = _fast()
