@@ -274,7 +274,7 @@ def _plan_step(state, length, new, n_rows):
     served = fits & paged & roomy
     comes = served.unsqueeze(1) & (j >= held.unsqueeze(1)) & (j < need.unsqueeze(1))
     taken = torch.cumsum(comes.flatten(), 0).view_as(comes)
-    table = torch.where(comes, free[(there - taken).clamp(min=0)], torch.where(goes, -1, pages))
+    table = torch.where(comes, free[(there - taken).clamp(0, free.shape[0] - 1)], torch.where(goes, -1, pages))
     held = torch.where(served | (need < held) & fits, need, held)
     rows = torch.where(served, new, 0)
     kv_len = torch.where(served, length + new, torch.minimum(length, held * page))
