@@ -15,8 +15,8 @@
 // CTAs an SM keep about 190 KB in flight there.  A sequence is split over several CTAs
 // where there are too few for the SMs; a second kernel, started while the first
 // one runs, joins their shares.  Measured: 64 sequences of up to 4000 positions, 7
-// rows, 16 / 8 heads x 128: 133 us, 6.0 TB/s (88 % of a copy's rate; 512 CTAs in
-// not quite two waves); one row over a window of 4096, 32 / 8 heads: 9.2 us, a
+// rows, 16 / 8 heads x 128: 134 us, 5.9 TB/s (88 % of a copy's rate; 512 CTAs in
+// not quite two waves); one row over a window of 4096, 32 / 8 heads: 9.7 us, a
 // chain of latencies (lengths, pages, tiles, two products, join).
 //
 // Weights enter the product with the values as a sum of two 16-bit numbers (16
@@ -24,7 +24,7 @@
 // steps of 2^-39 of the largest): the second MMA hides behind the copies.
 // Blocks of 64 rows (256 channels only) are bound by the MMAs: one number there,
 // as in the tiles of cp_kv16_prompt.cu (two are half as many MMAs again).  2048
-// rows over 4096 positions, 16 / 4 heads x 256: 766 us, 135 TFLOP/s, about what
+// rows over 4096 positions, 16 / 4 heads x 256: 770 us, 134 TFLOP/s, about what
 // mma.sync gives on this card; 1246 us with each load right before its product.
 //
 // A position that a row does not see never reaches it: its score is replaced

@@ -37,8 +37,8 @@
 // Every wait is bounded; one that runs out ends all roles, and the CTA with them
 // once its copies and MMAs in flight are through.
 //
-// Measured: 8192 rows over 16384 positions, window 4096, 32 / 8 heads x 128: 472
-// us, 1167 TFLOP/s (59 % of the burst rate).  A turn of both blocks of rows takes
+// Measured: 8192 rows over 16384 positions, window 4096, 32 / 8 heads x 128: 467
+// us, 1178 TFLOP/s (62 % of the burst rate).  A turn of both blocks of rows takes
 // 2550 to 2700 clocks, of which the MMAs are 2048; what is left is the way from a
 // block's last weights to its next scores (commit, barrier, wake-up: about 500).
 // The steps there: one warp issuing for both products 647 us, a warp each with the
